@@ -225,6 +225,7 @@ dfw_status dfw_check(void *cuda_stream);
 #define DFW_ST_RANGE 4u   /* plan offsets out of order or out of range */
 #define DFW_ST_TIMEOUT 8u /* a wait for a bulk copy gave up; the kernel returned early */
 #define DFW_ST_CHECK 16u  /* checks build only: an index or copy range left its buffer (the access was skipped) */
+#define DFW_ST_INDEX 32u  /* a token id past the table's last row (its output row is zero; its gradient is left out) */
 
 /*
  * dfw_status_bits -- dfw_check, and the status bits it read and cleared in
@@ -653,6 +654,144 @@ dfw_status dfw_rans_encode(const uint16_t *const *tensors, const uint64_t *sizes
  */
 dfw_status dfw_rans_decode(const uint8_t *d_stream, const uint8_t *d_mant, const uint64_t *d_block_start,
                            const dfw_rans_table *table, uint16_t *d_out, void *cuda_stream);
+
+/*
+ * 4-BIT WEIGHTS -- the lossy neighbour of dfw_decode_gemv_lanes, for matrices
+ * that may lose precision: the LazyWeights write-up's group-quantised integer
+ * weights, uncoded.  A rows x cols matrix has whole codes q in 0..15, one
+ * scale s (bf16) and, with zeros, one zero point z in 0..15 per row and group
+ * of `group` consecutive columns:
+ *   w[n, k] = s[n, k / group] (q[n, k] - z[n, k / group]),  z = 8 without zeros
+ * (4.125 to 4.75 bits per weight).  The packed form is the library's own
+ * (tiles of 16 rows x 128 columns, each contiguous with its scales and zero
+ * points); make it with dfw_q4_pack or dfw_q4_quantise.
+ */
+typedef struct dfw_q4_info {
+    uint32_t rows;  /* 1..2^30 */
+    uint32_t cols;  /* a multiple of group, at most DFW_Q4_MAX_COLS */
+    uint32_t group; /* 32, 64 or 128 */
+    uint32_t zeros; /* 1: the groups have zero points */
+    uint64_t bytes; /* length of the packed form (dfw_q4_query) */
+} dfw_q4_info;
+
+#define DFW_Q4_MAX_COLS 65536
+#define DFW_Q4_MAX_VECTORS 64
+
+/* dfw_q4_query -- fills info->bytes from the other fields.  Host only.
+ * Errors: DFW_EINVAL (unsupported shape). */
+dfw_status dfw_q4_query(dfw_q4_info *info);
+
+/*
+ * dfw_q4_pack -- packs a matrix that is 4-bit already.  Asynchronous.
+ *   d_codes   device, rows x cols / 2 bytes, row-major: byte j of a row holds
+ *             column 2 j in its low and column 2 j + 1 in its high half;
+ *             4-byte aligned
+ *   d_scales  device, rows x cols / group bf16, row-major
+ *   d_zeros   device, rows x cols / group bytes (the low four bits count);
+ *             NULL exactly when info->zeros is 0
+ *   d_packed  device, info->bytes, 16-byte aligned (output)
+ * Errors: DFW_EINVAL, DFW_EALIGN, DFW_ECUDA.
+ */
+dfw_status dfw_q4_pack(const uint8_t *d_codes, const uint16_t *d_scales, const uint8_t *d_zeros,
+                       const dfw_q4_info *info, uint8_t *d_packed, void *cuda_stream);
+
+/*
+ * dfw_q4_quantise -- rounds bf16 weights (a decoded tensor) to 4 bits and
+ * packs them.  Per group, with fp32 arithmetic rounded to nearest even:
+ *   without zeros  s = bf16(max |w| / 7),  q = clamp(round(w / s), -8, 7) + 8
+ *   with zeros     lo = min(w, 0), hi = max(w, 0), s = bf16(hi / 15 - lo / 15),
+ *                  z = clamp(round(-lo / s), 0, 15), q = clamp(round(w / s) + z, 0, 15)
+ * A group whose scale is 0 has q = z (z = 0 with zeros); a group that holds
+ * an infinity or NaN has scale NaN and q = z.  Asynchronous.
+ *   d_w   device, bf16, row n at d_w + n ldw (ldw >= cols elements)
+ * Errors: DFW_EINVAL, DFW_EALIGN, DFW_ECUDA.
+ */
+dfw_status dfw_q4_quantise(const uint16_t *d_w, uint64_t ldw, const dfw_q4_info *info, uint8_t *d_packed,
+                           void *cuda_stream);
+
+/*
+ * dfw_q4_dequantise -- the packed matrix as bf16, row-major rows x cols:
+ * s (q - z), rounded once.  For inspection, and for products with more than
+ * DFW_Q4_MAX_VECTORS vectors.  d_out 16-byte aligned.  Asynchronous.
+ * Errors: DFW_EINVAL, DFW_EALIGN, DFW_ECUDA.
+ */
+dfw_status dfw_q4_dequantise(const uint8_t *d_packed, const dfw_q4_info *info, uint16_t *d_out, void *cuda_stream);
+
+/*
+ * dfw_q4_gemv -- y_j = W x_j for m vectors (the tokens of one step), straight
+ * from the packed form.  Source: as dfw_decode_gemv_lanes (weights stay
+ * compressed up to the compute units).
+ *   m      0..DFW_Q4_MAX_VECTORS (0 does nothing)
+ *   d_x    device, bf16, vector j at d_x + j ldx (ldx >= cols for m > 1)
+ *   d_y    device, result j at element j ldy (ldy >= rows for m > 1): fp32
+ *          if y_fp32 is 1, else bf16
+ * Arithmetic: (q - z) and x are exact in bf16 and their products exact; a
+ * group's products are summed in fp32, the sums multiplied by their scales
+ * and added in fp32, in an order fixed by the shape (repeated calls give
+ * identical bits); a bf16 result is rounded once.  Asynchronous; needs no
+ * scratch.  Errors: DFW_EINVAL, DFW_EALIGN (d_packed 16 bytes, d_x and d_y
+ * their element), DFW_ECUDA.
+ */
+dfw_status dfw_q4_gemv(const uint8_t *d_packed, const dfw_q4_info *info, uint32_t m, const uint16_t *d_x,
+                       uint64_t ldx, void *d_y, int y_fp32, uint64_t ldy, void *cuda_stream);
+
+/*
+ * EMBEDDING ROWS -- the rows of a rows x dim table that token ids name,
+ * scaled: out[t, :] = bf16(scale table[id[t], :]), one rounding to nearest
+ * even (scale 1 keeps the bit patterns).  A negative id is padding: its row
+ * is zero.  An id of rows or more gives a zero row too and is reported
+ * through dfw_check (DFW_ST_INDEX).  Ids are 32-bit integers, or 64-bit with
+ * ids64 = 1.  Asynchronous.
+ *
+ * dfw_embed_lanes -- the table is entropy-coded: weights [first, first + rows
+ * dim) of a scope with its known-start plan (the chunks a row needs are
+ * decoded, nothing else is read; a row may start anywhere in a chunk).
+ * Source: DFloat11 abstract point (iii), decompression of a part of the
+ * model on demand; the LazyWeights write-up (lanes with known starts).
+ *   scope    as for dfw_decode_lanes_seq; a group found corrupt writes
+ *            nothing and is reported through dfw_check
+ *   d_out    device, bf16, row t at d_out + t ld_out (ld_out >= dim)
+ * dfw_embed_rows -- the table is bf16 (a decoded scope): row v at
+ * d_table + v ld_table (ld_table >= dim).
+ * Limits: tokens <= DFW_EMBED_MAX_TOKENS, rows <= DFW_EMBED_MAX_ROWS, dim <=
+ * DFW_EMBED_MAX_DIM.  Errors: DFW_EINVAL, DFW_EALIGN (ids and bf16 pointers
+ * to their element, the scope's buffers as dfw_decode_lanes), DFW_ECUDA.
+ */
+#define DFW_EMBED_MAX_TOKENS 1048576u
+#define DFW_EMBED_MAX_ROWS 1073741824u
+#define DFW_EMBED_MAX_DIM 1048576u
+
+dfw_status dfw_embed_lanes(const dfw_lanes_scope *scope, uint64_t first, uint64_t rows, uint32_t dim,
+                           const void *d_ids, int ids64, uint64_t tokens, float scale, uint16_t *d_out,
+                           uint64_t ld_out, void *cuda_stream);
+
+dfw_status dfw_embed_rows(const uint16_t *d_table, uint64_t rows, uint32_t dim, uint64_t ld_table, const void *d_ids,
+                          int ids64, uint64_t tokens, float scale, uint16_t *d_out, uint64_t ld_out,
+                          void *cuda_stream);
+
+/*
+ * dfw_embed_grad -- the gradient of the table: grad[v, :] = scale times the
+ * sum of dy[t, :] over the tokens t with id v.  Padding ids and ids past the
+ * table (reported through dfw_check) are left out.  Sums are fp32, their
+ * order fixed by the ids and the shape (the tokens are sorted by id, a row's
+ * tokens stay in order), so repeated calls give identical bits.  The result
+ * can update a decoded table, which dfw_encode_device codes again.
+ *   d_dy        device, fp32 if dy_fp32 is 1, else bf16; row t at t ld_dy
+ *   d_grad      device, rows x dim, contiguous, fp32 if grad_fp32 is 1, else
+ *               bf16.  accumulate 0: every row is written (zeros where no
+ *               token points).  accumulate 1: rows that tokens point to are
+ *               added to, one rounding per element and call; others are not touched
+ *   d_scratch   device, 16-byte aligned, scratch_bytes >=
+ *               dfw_embed_grad_scratch_bytes(tokens, dim); calls that overlap
+ *               in time need one each
+ * d_grad must not overlap an input.  Limits as above.  Asynchronous.
+ * Errors: DFW_EINVAL, DFW_EALIGN, DFW_ENOMEM (scratch too small), DFW_ECUDA.
+ */
+uint64_t dfw_embed_grad_scratch_bytes(uint64_t tokens, uint32_t dim);
+
+dfw_status dfw_embed_grad(const void *d_ids, int ids64, uint64_t tokens, const void *d_dy, int dy_fp32,
+                          uint64_t ld_dy, uint64_t rows, uint32_t dim, float scale, void *d_grad, int grad_fp32,
+                          int accumulate, void *d_scratch, uint64_t scratch_bytes, void *cuda_stream);
 
 /* Static English text for a status code. */
 const char *dfw_strerror(dfw_status status);

@@ -21,13 +21,16 @@ from dataclasses import dataclass
 import numpy as np
 import torch
 
-from ._abi import (EALIGN, ECAP, ECORRUPT, ECUDA, EINVAL, ENOMEM, OK, ST_COUNT, ST_LUT, ST_RANGE, ST_TIMEOUT,
-                   ContainerView, DfwError, EncodeScope, LanesInfo, LanesScope, PlanInfo, RansTable, Table, check as _check, lib)
+from ._abi import (EALIGN, ECAP, ECORRUPT, ECUDA, EINVAL, ENOMEM, OK, ST_COUNT, ST_INDEX, ST_LUT, ST_RANGE,
+                   ST_TIMEOUT, ContainerView, DfwError, EncodeScope, LanesInfo, LanesScope, PlanInfo, Q4Info, RansTable, Table,
+                   check as _check, lib)
 
 __all__ = ["encode", "encode_multi", "plan", "DeviceCompressed", "decode", "decode_block", "check",
            "plan_lanes", "LanesPlan", "DeviceLanes", "decode_lanes", "decode_lanes_seq", "LanesInfo",
            "encode_device", "encode_device_multi", "encode_device_scratch_bytes", "decode_gemv_lanes",
            "rans_encode", "RansEncoded", "DeviceRans", "rans_decode", "RansTable", "save", "load",
+           "Q4Weights", "q4_pack", "q4_quantise", "q4_dequantise", "q4_gemv", "embed_lanes", "embed_rows", "embed_grad",
+           "embed_grad_scratch_bytes",
            "Encoded", "Plan", "Table", "PlanInfo", "DfwError", "lib", "mant_bytes", "stream_bound",
            "OK", "EINVAL", "ECAP", "ENOMEM", "ECORRUPT", "EALIGN", "ECUDA"]
 
@@ -515,10 +518,243 @@ def check_status(stream=None) -> int:
 
 def status_bits(stream=None) -> tuple[int, int]:
     """(status, bits): dfw_check's result and the device status bits it read
-    and cleared (ST_COUNT, ST_LUT, ST_RANGE, ST_TIMEOUT)."""
+    and cleared (ST_COUNT, ST_LUT, ST_RANGE, ST_TIMEOUT, ST_INDEX)."""
     bits = ctypes.c_uint32(0)
     st = int(lib().dfw_status_bits(_stream_handle(stream), ctypes.byref(bits)))
     return st, int(bits.value)
+
+
+# ------------------------------------------- 4-bit weights and embedding rows
+
+class _On:
+    """Makes a tensor's device current, and ``stream`` if one is given (so
+    that what the call allocates belongs to it), for one library call."""
+    __slots__ = ("ctx",)
+
+    def __init__(self, device: torch.device, stream):
+        if stream is not None:
+            if stream.device != device:
+                raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+            self.ctx = torch.cuda.stream(stream)
+        else:
+            self.ctx = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return _stream_handle(None)
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def _expect(name: str, t: torch.Tensor, device: torch.device, dtypes, dim: int | None = None) -> None:
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be on {device if device.type == 'cuda' else 'a CUDA device'}, not {t.device}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
+    if dim is not None and (t.dim() != dim or (t.numel() and t.stride(-1) != 1)):
+        raise ValueError(f"{name} must have {dim} dimensions, the last one contiguous")
+
+
+def _ld(t: torch.Tensor, width: int) -> int:
+    """Elements from one row to the next (a single row's is not used)."""
+    return t.stride(0) if t.shape[0] > 1 else width
+
+
+_BF16, _F32 = (torch.bfloat16,), (torch.float32,)
+_FLOATS, _IDS, _BYTES = (torch.bfloat16, torch.float32), (torch.int32, torch.int64), (torch.uint8,)
+
+
+@dataclass
+class Q4Weights:
+    """A matrix held in 4 bits with group scales (``dfw_q4_info``), packed."""
+    packed: torch.Tensor  # uint8[info.bytes]
+    info: Q4Info
+
+    @property
+    def shape(self) -> tuple[int, int]:
+        return int(self.info.rows), int(self.info.cols)
+
+    @property
+    def group(self) -> int:
+        return int(self.info.group)
+
+    @property
+    def zeros(self) -> bool:
+        return bool(self.info.zeros)
+
+
+def _q4_new(rows: int, cols: int, group: int, zeros: bool, device) -> Q4Weights:
+    if not (0 < rows < 1 << 32 and 0 < cols < 1 << 32 and 0 < group < 1 << 32):
+        raise DfwError(EINVAL, "dfw_q4_query")
+    info = Q4Info(rows, cols, group, int(zeros), 0)
+    _check(lib().dfw_q4_query(ctypes.byref(info)), "dfw_q4_query")
+    return Q4Weights(torch.empty(int(info.bytes), dtype=torch.uint8, device=device), info)
+
+
+def q4_pack(codes: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor | None = None, group: int = 128,
+            stream=None) -> Q4Weights:
+    """Packs a matrix that is 4-bit already (``dfw_q4_pack``): ``codes`` uint8
+    [rows, cols / 2] (even column in the low half), ``scales`` bf16 and
+    ``zeros`` uint8 (or None) [rows, cols / group], all contiguous."""
+    dev = codes.device
+    _expect("codes", codes, dev, _BYTES, 2)
+    rows, cols = codes.shape[0], 2 * codes.shape[1]
+    for name, t, dtypes in (("scales", scales, _BF16), ("zeros", zeros, _BYTES)):
+        if t is not None:
+            _expect(name, t, dev, dtypes, 2)
+            if t.shape[0] != rows or t.shape[1] * group != cols or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous [{rows}, {cols} / {group}] tensor")
+    if not codes.is_contiguous():
+        raise ValueError("codes must be contiguous")
+    with _On(dev, stream) as sh:
+        q = _q4_new(rows, cols, group, zeros is not None, dev)
+        _check(lib().dfw_q4_pack(codes.data_ptr(), scales.data_ptr(), None if zeros is None else zeros.data_ptr(),
+                                 ctypes.byref(q.info), q.packed.data_ptr(), sh), "dfw_q4_pack")
+    return q
+
+
+def q4_quantise(w: torch.Tensor, group: int = 128, zeros: bool = False, stream=None) -> Q4Weights:
+    """Rounds a bf16 matrix [rows, cols] (a decoded tensor's view) to 4 bits
+    with a scale, and with ``zeros`` a zero point, per row and ``group``
+    columns (``dfw_q4_quantise``)."""
+    _expect("w", w, w.device, _BF16, 2)
+    with _On(w.device, stream) as sh:
+        q = _q4_new(w.shape[0], w.shape[1], group, zeros, w.device)
+        _check(lib().dfw_q4_quantise(w.data_ptr(), _ld(w, w.shape[1]), ctypes.byref(q.info), q.packed.data_ptr(), sh),
+               "dfw_q4_quantise")
+    return q
+
+
+def q4_dequantise(q: Q4Weights, stream=None) -> torch.Tensor:
+    """The bf16 matrix [rows, cols] that ``q`` stands for (``dfw_q4_dequantise``)."""
+    with _On(q.packed.device, stream) as sh:
+        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.packed.device)
+        _check(lib().dfw_q4_dequantise(q.packed.data_ptr(), ctypes.byref(q.info), out.data_ptr(), sh), "dfw_q4_dequantise")
+    return out
+
+
+def q4_gemv(q: Q4Weights, x: torch.Tensor, out: torch.Tensor | None = None, out_dtype=torch.float32,
+            stream=None) -> torch.Tensor:
+    """y = x W^T for the few vectors of one step (``dfw_q4_gemv``): ``x`` bf16
+    [tokens, cols] or [cols], at most 64 tokens; returns fp32 or bf16
+    [tokens, rows] or [rows].  Several matrices with the same input (q, k, v;
+    gate, up) are best held as one, their rows one below the other."""
+    dev = q.packed.device
+    rows, cols = q.shape
+    _expect("x", x, dev, _BF16, x.dim() if x.dim() in (1, 2) else 2)
+    if x.shape[-1] != cols:
+        raise ValueError(f"x has {x.shape[-1]} columns, the matrix {cols}")
+    x2 = x if x.dim() == 2 else x[None]
+    m = x2.shape[0]
+    with _On(dev, stream) as sh:
+        if out is None:
+            if out_dtype not in _FLOATS:
+                raise TypeError(f"out_dtype {out_dtype}, expected one of {_FLOATS}")
+            out = torch.empty((*x.shape[:-1], rows), dtype=out_dtype, device=dev)
+        else:
+            _expect("out", out, dev, _FLOATS, x.dim())
+            if out.shape != (*x.shape[:-1], rows):
+                raise ValueError(f"out must have shape {(*x.shape[:-1], rows)}")
+        _check(lib().dfw_q4_gemv(q.packed.data_ptr(), ctypes.byref(q.info), m, x2.data_ptr(), _ld(x2, cols),
+                                 out.data_ptr(), int(out.dtype == torch.float32),
+                                 out.stride(0) if x.dim() == 2 and m > 1 else rows, sh), "dfw_q4_gemv")
+    return out
+
+
+def _embed_out(ids: torch.Tensor, dim: int, out, dev) -> torch.Tensor:
+    _expect("ids", ids, dev, _IDS)
+    if not ids.is_contiguous():
+        raise ValueError("ids must be contiguous")
+    if out is None:
+        return torch.empty((*ids.shape, dim), dtype=torch.bfloat16, device=dev)
+    _expect("out", out, dev, _BF16)
+    if out.shape != (*ids.shape, dim) or (out.numel() and out.stride(-1) != 1) or (out.dim() != 2 and not out.is_contiguous()):
+        raise ValueError(f"out must have shape {(*ids.shape, dim)}, contiguous (or 2-dimensional with contiguous rows)")
+    return out
+
+
+def _out_ld(out: torch.Tensor, dim: int) -> int:
+    return out.stride(0) if out.dim() == 2 and out.shape[0] > 1 else dim
+
+
+def embed_lanes(dl: DeviceLanes, ids: torch.Tensor, dim: int, scale: float = 1.0, first: int = 0,
+                rows: int | None = None, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Rows of an entropy-coded embedding table by token id, scaled
+    (``dfw_embed_lanes``): only the chunks those rows need are decoded.  The
+    table is weights [first, first + rows dim) of the scope (by default all
+    whole rows from ``first``).  ``ids``: int32 or int64, any shape, negative =
+    padding (a zero row); returns bf16 [*ids.shape, dim]."""
+    dev = dl.mant.device
+    if rows is None:
+        rows = (dl.n - first) // dim if dim > 0 else 0
+    with _On(dev, stream) as sh:
+        out = _embed_out(ids, dim, out, dev)
+        scope = LanesScope(_ptr(dl.stream), _ptr(dl.mant), _ptr(dl.lut), _ptr(dl.chunk_bits), _ptr(dl.group_start),
+                           ctypes.pointer(dl.table), ctypes.pointer(dl.info))
+        _check(lib().dfw_embed_lanes(ctypes.byref(scope), first, rows, dim, ids.data_ptr(), int(ids.dtype == torch.int64),
+                                     ids.numel(), scale, out.data_ptr(), _out_ld(out, dim), sh), "dfw_embed_lanes")
+    return out
+
+
+def embed_rows(table: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, out: torch.Tensor | None = None,
+               stream=None) -> torch.Tensor:
+    """Rows of a bf16 embedding table [rows, dim] (a decoded scope's view) by
+    token id, scaled (``dfw_embed_rows``); ids and result as :func:`embed_lanes`."""
+    dev = table.device
+    _expect("table", table, dev, _BF16, 2)
+    rows, dim = table.shape
+    with _On(dev, stream) as sh:
+        out = _embed_out(ids, dim, out, dev)
+        _check(lib().dfw_embed_rows(table.data_ptr(), rows, dim, _ld(table, dim), ids.data_ptr(),
+                                    int(ids.dtype == torch.int64), ids.numel(), scale, out.data_ptr(),
+                                    _out_ld(out, dim), sh), "dfw_embed_rows")
+    return out
+
+
+def embed_grad(ids: torch.Tensor, dy: torch.Tensor, rows: int, scale: float = 1.0, out: torch.Tensor | None = None,
+               out_dtype=torch.float32, accumulate: bool = False, scratch: torch.Tensor | None = None,
+               stream=None) -> torch.Tensor:
+    """Gradient of an embedding table of ``rows`` rows (``dfw_embed_grad``):
+    row v gets ``scale`` times the sum of ``dy``'s rows whose id is v.  ``dy``:
+    bf16 or fp32 [*ids.shape, dim].  Returns fp32 or bf16 [rows, dim]; with
+    ``accumulate`` it is added to ``out``, and rows without tokens stay as they
+    are.  ``scratch`` (uint8, ``embed_grad_scratch_bytes``) may be passed to
+    reuse one buffer; calls that overlap in time need one each."""
+    dev = dy.device
+    _expect("dy", dy, dev, _FLOATS)
+    _expect("ids", ids, dev, _IDS)
+    if dy.dim() != ids.dim() + 1 or dy.shape[:-1] != ids.shape or not ids.is_contiguous():
+        raise ValueError("dy must have one row per id, ids must be contiguous")
+    if (dy.numel() and dy.stride(-1) != 1) or (dy.dim() != 2 and not dy.is_contiguous()):
+        raise ValueError("dy must be contiguous (or 2-dimensional with contiguous rows)")
+    tokens, dim = ids.numel(), dy.shape[-1]
+    with _On(dev, stream) as sh:
+        if out is None:
+            if accumulate:
+                raise ValueError("accumulate needs an out tensor")
+            if out_dtype not in _FLOATS:
+                raise TypeError(f"out_dtype {out_dtype}, expected one of {_FLOATS}")
+            out = torch.empty((rows, dim), dtype=out_dtype, device=dev)
+        else:
+            _expect("out", out, dev, _FLOATS)
+            if out.shape != (rows, dim) or not out.is_contiguous():
+                raise ValueError(f"out must be a contiguous [{rows}, {dim}] tensor")
+        if scratch is None:
+            scratch = torch.empty(embed_grad_scratch_bytes(tokens, dim), dtype=torch.uint8, device=dev)
+        else:
+            _expect("scratch", scratch, dev, _BYTES, 1)
+        _check(lib().dfw_embed_grad(ids.data_ptr(), int(ids.dtype == torch.int64), tokens, dy.data_ptr(),
+                                    int(dy.dtype == torch.float32), _out_ld(dy, dim), rows, dim, scale, out.data_ptr(),
+                                    int(out.dtype == torch.float32), int(accumulate), scratch.data_ptr(),
+                                    scratch.numel(), sh), "dfw_embed_grad")
+    return out
+
+
+def embed_grad_scratch_bytes(tokens: int, dim: int) -> int:
+    return int(lib().dfw_embed_grad_scratch_bytes(tokens, dim))
 
 
 # ------------------------------------------------------------------ container

@@ -8,7 +8,7 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libdfw.so")
 
 OK, EINVAL, ECAP, ENOMEM, ECORRUPT, EALIGN, ECUDA = range(7)
-ST_COUNT, ST_LUT, ST_RANGE, ST_TIMEOUT, ST_CHECK = 1, 2, 4, 8, 16  # device status bits (include/dfw.h DFW_ST_*)
+ST_COUNT, ST_LUT, ST_RANGE, ST_TIMEOUT, ST_CHECK, ST_INDEX = 1, 2, 4, 8, 16, 32  # device status bits (include/dfw.h DFW_ST_*)
 FORMAT_VERSION = 1
 MAX_CAP = 32
 
@@ -67,12 +67,19 @@ class RansTable(ctypes.Structure):
                 ("reserved", ctypes.c_uint32), ("freq", ctypes.c_uint16 * 256)]
 
 
+class Q4Info(ctypes.Structure):
+    """dfw_q4_info: the shape of a 4-bit matrix."""
+    _fields_ = [("rows", ctypes.c_uint32), ("cols", ctypes.c_uint32), ("group", ctypes.c_uint32),
+                ("zeros", ctypes.c_uint32), ("bytes", ctypes.c_uint64)]
+
+
 _lib = None
 
 # name -> (restype, argtypes); the symbols include/dfw.h declares
 _vp, _u64, _i = ctypes.c_void_p, ctypes.c_uint64, ctypes.c_int
 _TP, _IP, _LP = ctypes.POINTER(Table), ctypes.POINTER(PlanInfo), ctypes.POINTER(LanesInfo)
 _RP = ctypes.POINTER(RansTable)
+_QP = ctypes.POINTER(Q4Info)
 SIGNATURES = {
     "dfw_stream_bound": (_u64, [_u64]),
     "dfw_mant_bytes": (_u64, [_u64]),
@@ -104,6 +111,16 @@ SIGNATURES = {
     "dfw_rans_stream_bound": (_u64, [_u64]),
     "dfw_rans_encode": (_i, [_vp, _vp, _i, _vp, _u64, _vp, _u64, _vp, _RP, _i]),
     "dfw_rans_decode": (_i, [_vp, _vp, _vp, _RP, _vp, _vp]),
+    "dfw_q4_query": (_i, [_QP]),
+    "dfw_q4_pack": (_i, [_vp, _vp, _vp, _QP, _vp, _vp]),
+    "dfw_q4_quantise": (_i, [_vp, _u64, _QP, _vp, _vp]),
+    "dfw_q4_dequantise": (_i, [_vp, _QP, _vp, _vp]),
+    "dfw_q4_gemv": (_i, [_vp, _QP, ctypes.c_uint32, _vp, _u64, _vp, _i, _u64, _vp]),
+    "dfw_embed_lanes": (_i, [_vp, _u64, _u64, ctypes.c_uint32, _vp, _i, _u64, ctypes.c_float, _vp, _u64, _vp]),
+    "dfw_embed_rows": (_i, [_vp, _u64, ctypes.c_uint32, _u64, _vp, _i, _u64, ctypes.c_float, _vp, _u64, _vp]),
+    "dfw_embed_grad_scratch_bytes": (_u64, [_u64, ctypes.c_uint32]),
+    "dfw_embed_grad": (_i, [_vp, _i, _u64, _vp, _i, _u64, _u64, ctypes.c_uint32, ctypes.c_float, _vp, _i, _i, _vp, _u64,
+                            _vp]),
     "dfw_check": (_i, [_vp]),
     "dfw_strerror": (ctypes.c_char_p, [_i]),
 }

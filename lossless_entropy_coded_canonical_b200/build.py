@@ -19,7 +19,8 @@ LIB = os.path.join(PKG, "libdfw.so")
 # the kernels compute is checked before use (DFW_CHECKS)
 LIB_CHECKS = os.path.join(PKG, "libdfw_checks.so")
 SOURCES = ["dfw_host.cpp", "dfw_decode.cu", "dfw_encode.cu", "dfw_rans.cpp"]
-HEADERS = ["dfw_internal.h", "dfw_device.cuh", "dfw_lanes.cuh", "dfw_rans.cuh", os.path.join("..", "..", "include", "dfw.h")]
+HEADERS = ["dfw_internal.h", "dfw_device.cuh", "dfw_lanes.cuh", "dfw_rans.cuh", "dfw_q4.cuh", "dfw_embed.cuh",
+           os.path.join("..", "..", "include", "dfw.h")]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

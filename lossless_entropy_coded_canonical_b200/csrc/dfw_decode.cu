@@ -46,6 +46,8 @@ __device__ unsigned int g_check_site;  // checks build: the first range check th
 #include "dfw_device.cuh"
 #include "dfw_lanes.cuh"
 #include "dfw_rans.cuh"
+#include "dfw_q4.cuh"
+#include "dfw_embed.cuh"
 
 namespace dfw {
 namespace {
@@ -546,6 +548,66 @@ extern "C" dfw_status dfw_rans_decode(const uint8_t *d_stream, const uint8_t *d_
         return DFW_ECUDA;
     return launch_rans_decode(d_stream, d_mant, d_block_start, table, d_out, static_cast<cudaStream_t>(cuda_stream),
                               sms);
+}
+
+extern "C" dfw_status dfw_q4_query(dfw_q4_info *info) {
+    Q4Params p;
+    if (!info || !q4_shape(info, p)) return DFW_EINVAL;
+    info->bytes = p.row_tiles * p.col_tiles * p.tile_bytes;
+    return DFW_OK;
+}
+
+extern "C" dfw_status dfw_q4_pack(const uint8_t *d_codes, const uint16_t *d_scales, const uint8_t *d_zeros,
+                                  const dfw_q4_info *info, uint8_t *d_packed, void *cuda_stream) {
+    dfw::NvtxRange nvtx_range("dfw_q4_pack");
+    return launch_q4_pack(d_codes, d_scales, d_zeros, info, d_packed, static_cast<cudaStream_t>(cuda_stream));
+}
+
+extern "C" dfw_status dfw_q4_quantise(const uint16_t *d_w, uint64_t ldw, const dfw_q4_info *info, uint8_t *d_packed,
+                                      void *cuda_stream) {
+    dfw::NvtxRange nvtx_range("dfw_q4_quantise");
+    return launch_q4_quantise(d_w, ldw, info, d_packed, static_cast<cudaStream_t>(cuda_stream));
+}
+
+extern "C" dfw_status dfw_q4_dequantise(const uint8_t *d_packed, const dfw_q4_info *info, uint16_t *d_out,
+                                        void *cuda_stream) {
+    dfw::NvtxRange nvtx_range("dfw_q4_dequantise");
+    return launch_q4_dequantise(d_packed, info, d_out, static_cast<cudaStream_t>(cuda_stream));
+}
+
+extern "C" dfw_status dfw_q4_gemv(const uint8_t *d_packed, const dfw_q4_info *info, uint32_t m, const uint16_t *d_x,
+                                  uint64_t ldx, void *d_y, int y_fp32, uint64_t ldy, void *cuda_stream) {
+    dfw::NvtxRange nvtx_range("dfw_q4_gemv");
+    return launch_q4_gemv(d_packed, info, m, d_x, ldx, d_y, y_fp32, ldy, static_cast<cudaStream_t>(cuda_stream));
+}
+
+extern "C" dfw_status dfw_embed_lanes(const dfw_lanes_scope *scope, uint64_t first, uint64_t rows, uint32_t dim,
+                                      const void *d_ids, int ids64, uint64_t tokens, float scale, uint16_t *d_out,
+                                      uint64_t ld_out, void *cuda_stream) {
+    dfw::NvtxRange nvtx_range("dfw_embed_lanes");
+    return launch_embed_lanes(scope, first, rows, dim, d_ids, ids64, tokens, scale, d_out, ld_out,
+                              static_cast<cudaStream_t>(cuda_stream));
+}
+
+extern "C" dfw_status dfw_embed_rows(const uint16_t *d_table, uint64_t rows, uint32_t dim, uint64_t ld_table,
+                                     const void *d_ids, int ids64, uint64_t tokens, float scale, uint16_t *d_out,
+                                     uint64_t ld_out, void *cuda_stream) {
+    dfw::NvtxRange nvtx_range("dfw_embed_rows");
+    return launch_embed_rows(d_table, rows, dim, ld_table, d_ids, ids64, tokens, scale, d_out, ld_out,
+                             static_cast<cudaStream_t>(cuda_stream));
+}
+
+extern "C" uint64_t dfw_embed_grad_scratch_bytes(uint64_t tokens, uint32_t dim) {
+    return embed_grad_scratch(tokens, dim);
+}
+
+extern "C" dfw_status dfw_embed_grad(const void *d_ids, int ids64, uint64_t tokens, const void *d_dy, int dy_fp32,
+                                     uint64_t ld_dy, uint64_t rows, uint32_t dim, float scale, void *d_grad,
+                                     int grad_fp32, int accumulate, void *d_scratch, uint64_t scratch_bytes,
+                                     void *cuda_stream) {
+    dfw::NvtxRange nvtx_range("dfw_embed_grad");
+    return launch_embed_grad(d_ids, ids64, tokens, d_dy, dy_fp32, ld_dy, rows, dim, scale, d_grad, grad_fp32,
+                             accumulate, d_scratch, scratch_bytes, static_cast<cudaStream_t>(cuda_stream));
 }
 
 extern "C" dfw_status dfw_status_bits(void *cuda_stream, uint32_t *bits) {

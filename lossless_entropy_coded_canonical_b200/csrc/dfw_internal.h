@@ -50,6 +50,7 @@ constexpr uint32_t ST_LUT = 2u;     // a LUT pointer left the table or a code ra
 constexpr uint32_t ST_RANGE = 4u;   // out_start out of order or beyond n, or tile too large
 constexpr uint32_t ST_TIMEOUT = 8u; // a wait for a bulk copy gave up (the kernel returned early)
 constexpr uint32_t ST_CHECK = 16u;  // checks build only: an index or range left its buffer (access skipped)
+constexpr uint32_t ST_INDEX = 32u;  // a token id past the embedding table's last row
 
 // Sites of the checks build's range checks (the first failing one is kept).
 enum CheckSite : uint32_t {
