@@ -13,6 +13,8 @@
 
 #include <cuda_bf16.h>
 
+#include <algorithm>
+
 #include "dfw_lanes.cuh"
 #include "dfw_q4.cuh"
 
@@ -177,53 +179,311 @@ __global__ void __launch_bounds__(128) embed_lanes_rows(const RowsOfLanes p) {
 
 // ------------------------------------------------------ the table's gradient
 
-struct GradParams {
+// Sorting.  A CTA sorts a block of up to 1024 IPT tokens by row, stably, in
+// shared memory: 8 bits a pass from the lowest, each warp ranking its own run
+// of tokens (equal digits of 32 tokens found by one match instruction, so no
+// atomics and a fixed order), then one scan over (digit, warp).  Tokens
+// without a row get key `rows` and end up behind all others.
+constexpr uint32_t SORT_THREADS = 1024, SORT_WARPS = 32, SORT_STRIDE = 257;
+
+struct SortParams {
     IdSource ids;
+    uint32_t *keys, *pos;  // per block: sorted keys and the tokens they belong to
+    uint32_t blocks, passes;
+    uint8_t *fill;         // zeroed meanwhile by the CTAs past the sorting ones (null: nothing)
+    uint64_t fill_bytes;
+};
+
+template <int IPT>
+constexpr uint32_t sort_smem() {
+    return SORT_WARPS * SORT_STRIDE * 4u + 32u * 4u + SORT_THREADS * IPT * 6u;
+}
+
+// Zeroes bytes [0, n) of p from the CTAs [first, gridDim.x).
+__device__ __forceinline__ void zero_fill(uint8_t *p, uint64_t n, uint32_t first) {
+    const uint64_t me = (uint64_t)(blockIdx.x - first) * blockDim.x + threadIdx.x;
+    const uint64_t all = (uint64_t)(gridDim.x - first) * blockDim.x;
+    const uint64_t head = min(n, (uint64_t)(-reinterpret_cast<uintptr_t>(p) & 31u));
+    const uint64_t body = (n - head) >> 5, tail = n - head - (body << 5);
+    if (me < head) p[me] = 0;
+    if (me < tail) p[n - 1u - me] = 0;
+    const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+    for (uint64_t i = me; i < body; i += all) stg256_cs(p + head + (i << 5), z, z);
+}
+
+template <int IPT>
+__global__ void __launch_bounds__(SORT_THREADS, 1) grad_sort(const SortParams p) {
+    if (blockIdx.x >= p.blocks) {
+        zero_fill(p.fill, p.fill_bytes, p.blocks);
+        return;
+    }
+    extern __shared__ __align__(16) uint8_t smem[];
+    uint32_t *cnt = reinterpret_cast<uint32_t *>(smem);  // [warp][digit], rows of SORT_STRIDE: a scan's reads hit 32 banks
+    uint32_t *sums = cnt + SORT_WARPS * SORT_STRIDE;
+    uint32_t *s_key = sums + 32;
+    uint16_t *s_pos = reinterpret_cast<uint16_t *>(s_key + SORT_THREADS * IPT);
+    const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
+    const uint32_t base = blockIdx.x * SORT_THREADS * IPT, run = warp * 32u * IPT + lane;
+    uint32_t key[IPT];
+    uint16_t pos[IPT];
+#pragma unroll
+    for (int j = 0; j < IPT; ++j) {
+        const uint32_t t = base + run + 32u * j;
+        uint64_t row = p.ids.rows;
+        pos[j] = (uint16_t)(run + 32u * j);
+        key[j] = 0xFFFFFFFFu;
+        if (t < p.ids.tokens) key[j] = token_row(p.ids, t, row, true) ? (uint32_t)row : (uint32_t)p.ids.rows;
+    }
+    for (uint32_t pass = 0; pass < p.passes; ++pass) {
+        const uint32_t shift = 8u * pass;
+        for (uint32_t i = lane; i < 256u; i += 32u) cnt[warp * SORT_STRIDE + i] = 0u;
+        __syncwarp();
+        uint16_t rank[IPT];
+#pragma unroll
+        for (int j = 0; j < IPT; ++j) {
+            const uint32_t d = (key[j] >> shift) & 255u;
+            const uint32_t same = __match_any_sync(0xFFFFFFFFu, d), leader = __ffs(same) - 1u;
+            uint32_t *c = cnt + warp * SORT_STRIDE + d;
+            uint32_t old = 0;
+            if (lane == leader) {
+                old = *c;
+                *c = old + __popc(same);
+            }
+            rank[j] = (uint16_t)(__shfl_sync(0xFFFFFFFFu, old, leader) + __popc(same & ((1u << lane) - 1u)));
+            __syncwarp();
+        }
+        __syncthreads();
+        // exclusive offsets in (digit, warp) order: thread i takes digit i / 4, warps 8 (i mod 4) .. + 7
+        uint32_t *mine = cnt + 8u * (tid & 3u) * SORT_STRIDE + (tid >> 2), sum = 0;
+#pragma unroll
+        for (uint32_t k = 0; k < 8u; ++k) {
+            const uint32_t v = mine[k * SORT_STRIDE];
+            mine[k * SORT_STRIDE] = sum;
+            sum += v;
+        }
+        uint32_t incl = sum;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+            if (lane >= (uint32_t)d) incl += y;
+        }
+        if (lane == 31u) sums[warp] = incl;
+        __syncthreads();
+        uint32_t before = sums[lane];
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, before, d);
+            if (lane >= (uint32_t)d) before += y;
+        }
+        before = __shfl_sync(0xFFFFFFFFu, before, (warp + 31u) & 31u);
+        const uint32_t off = (warp ? before : 0u) + incl - sum;
+#pragma unroll
+        for (uint32_t k = 0; k < 8u; ++k) mine[k * SORT_STRIDE] += off;
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < IPT; ++j) {
+            const uint32_t to = cnt[warp * SORT_STRIDE + ((key[j] >> shift) & 255u)] + rank[j];
+            s_key[to] = key[j];
+            s_pos[to] = pos[j];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < IPT; ++j) {
+            key[j] = s_key[run + 32u * j];
+            pos[j] = s_pos[run + 32u * j];
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < IPT; ++j) {
+        const uint32_t t = base + run + 32u * j;
+        if (t < p.ids.tokens) {
+            p.keys[t] = key[j];
+            p.pos[t] = base + pos[j];
+        }
+    }
+}
+
+// Joins sorted blocks into one order: a token's place is its place in its own
+// block plus, for every other block, how many of its keys come before (equal
+// keys of earlier blocks do, those of later ones do not).  LANES lanes share
+// a token's blocks, each a binary search.
+struct MergeParams {
+    const uint32_t *keys, *pos;
+    uint32_t *out_keys, *out_pos;
+    uint32_t tokens, blocks, block;
+};
+
+template <int LANES>
+__global__ void __launch_bounds__(256) grad_merge(const MergeParams p) {
+    const uint64_t i = (blockIdx.x * 256ull + threadIdx.x) / LANES;
+    const uint32_t sub = threadIdx.x % LANES;
+    const uint32_t t = (uint32_t)min(i, (uint64_t)p.tokens - 1u);
+    const uint32_t key = __ldg(p.keys + t), own = t / p.block;
+    uint32_t place = 0;
+    for (uint32_t b = sub; b < p.blocks; b += LANES) {
+        const uint32_t lo0 = b * p.block;
+        if (b == own) {
+            place += t - lo0;
+            continue;
+        }
+        uint32_t lo = lo0, hi = min(lo0 + p.block, p.tokens);
+        const uint32_t below = b < own ? key + 1u : key;  // keys are below 2^31
+        while (lo < hi) {
+            const uint32_t mid = (lo + hi) >> 1;
+            if (__ldg(p.keys + mid) < below) lo = mid + 1u;
+            else hi = mid;
+        }
+        place += lo - lo0;
+    }
+#pragma unroll
+    for (int d = 1; d < LANES; d <<= 1) place += __shfl_xor_sync(0xFFFFFFFFu, place, d);
+    if (sub == 0u && i < p.tokens) {
+        p.out_keys[place] = key;
+        p.out_pos[place] = __ldg(p.pos + t);
+    }
+}
+
+// Summing.  The sorted tokens are cut into windows of `window`; a thread
+// walks a window with VEC columns, eight rows of dy in flight, and writes a
+// row's sum when the next row's tokens begin.  A row whose tokens reach past
+// the window leaves a partial sum instead (slot 0 if it came from the window
+// before, else slot 1); grad_join adds those up in window order.
+struct ReduceParams {
+    const uint32_t *keys, *pos;
     const void *dy;
     void *grad;
+    float *partial;  // [windows][2][dim]
     uint64_t ld_dy;
-    uint32_t dim, dy_fp32, grad_fp32, accumulate;
+    uint32_t tokens, windows, window, dim, rows;
+    uint32_t tpr;          // threads per window (a power of two)
+    uint32_t col_blocks;
+    uint32_t accumulate;
     float scale;
 };
 
-// One CTA per table row: it scans the ids in order and adds the matching
-// tokens' rows, so the sum's order is fixed.
-__global__ void __launch_bounds__(256) embed_grad_scan(const GradParams p) {
-    __shared__ uint32_t s_hits[256 / 32];
-    for (uint64_t v = blockIdx.x; v < p.ids.rows; v += gridDim.x) {
-        for (uint32_t c0 = 0; c0 < p.dim; c0 += 256u) {
-            const uint32_t c = c0 + threadIdx.x;
-            float sum = 0.f;
-            bool any = false;
-            for (uint32_t t0 = 0; t0 < p.ids.tokens; t0 += 256u) {
-                const uint32_t t = t0 + threadIdx.x;
-                uint64_t row = 0;
-                const bool hit = t < p.ids.tokens && token_row(p.ids, t, row, v == 0u && c0 == 0u) && row == v;
-                const uint32_t m = __ballot_sync(0xFFFFFFFFu, hit);
-                if ((threadIdx.x & 31u) == 0u) s_hits[threadIdx.x >> 5] = m;
-                __syncthreads();
-                for (uint32_t q = 0; q < 8u; ++q)
-                    for (uint32_t b = s_hits[q]; b; b &= b - 1u) {
-                        const uint64_t at = (uint64_t)(t0 + 32u * q + __ffs(b) - 1u) * p.ld_dy + c;
-                        any = true;
-                        if (c < p.dim)
-                            sum += p.dy_fp32 ? static_cast<const float *>(p.dy)[at]
-                                             : __bfloat162float(static_cast<const __nv_bfloat16 *>(p.dy)[at]);
-                    }
-                __syncthreads();
+template <typename T>
+__device__ __forceinline__ float as_float(T v);
+template <>
+__device__ __forceinline__ float as_float<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ float as_float<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <typename T>
+__device__ __forceinline__ T from_float(float v);
+template <>
+__device__ __forceinline__ float from_float<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+template <typename T, int N>
+struct __align__(sizeof(T) * N) Pack {
+    T v[N];
+};
+
+// Writes (or adds) scale x sum to VEC columns of a row, rounded once.
+template <typename OUT, int VEC>
+__device__ __forceinline__ void put_row(void *grad, uint64_t at, const float (&acc)[VEC], float scale, bool add) {
+    constexpr int N = VEC * sizeof(OUT) > 16 ? 16 / sizeof(OUT) : VEC;  // at most 16 bytes at once
+#pragma unroll
+    for (int i = 0; i < VEC; i += N) {
+        Pack<OUT, N> *dst = reinterpret_cast<Pack<OUT, N> *>(static_cast<OUT *>(grad) + at + i);
+        Pack<OUT, N> o;
+        if (add) o = *dst;
+#pragma unroll
+        for (int j = 0; j < N; ++j) o.v[j] = from_float<OUT>(add ? fmaf(scale, acc[i + j], as_float<OUT>(o.v[j])) : scale * acc[i + j]);
+        *dst = o;
+    }
+}
+
+template <typename DY, typename OUT, int VEC>
+__global__ void __launch_bounds__(128) grad_reduce(const ReduceParams p) {
+    constexpr int U = 8;  // rows in flight
+    const uint32_t per = 128u / p.tpr;  // windows a CTA walks at once
+    const uint32_t w = blockIdx.x / p.col_blocks * per + threadIdx.x / p.tpr;
+    const uint32_t col = (blockIdx.x % p.col_blocks * p.tpr + threadIdx.x % p.tpr) * VEC;
+    if (w >= p.windows || col >= p.dim) return;
+    const uint32_t i0 = w * p.window, n = min(p.window, p.tokens - i0);
+    const uint32_t prev = i0 ? __ldg(p.keys + i0 - 1u) : 0xFFFFFFFFu;
+    const uint32_t next = i0 + n < p.tokens ? __ldg(p.keys + i0 + n) : 0xFFFFFFFFu;
+    float acc[VEC];
+    uint32_t cur = 0xFFFFFFFFu;  // the row being summed
+    bool first = true;           // its tokens began before the window, or at its first token
+    auto flush = [&](bool last) {
+        if (cur >= p.rows) return;
+        const bool left = first && cur == prev, right = last && cur == next;
+        if (left || right) {
+            float *dst = p.partial + ((uint64_t)w * 2u + (left ? 0u : 1u)) * p.dim + col;
+            constexpr int N = VEC > 4 ? 4 : VEC;
+#pragma unroll
+            for (int k = 0; k < VEC; k += N) {
+                Pack<float, N> o;
+#pragma unroll
+                for (int j = 0; j < N; ++j) o.v[j] = acc[k + j];
+                *reinterpret_cast<Pack<float, N> *>(dst + k) = o;
             }
-            if (c >= p.dim || (p.accumulate && !any)) continue;
-            float g = p.scale * sum;
-            const uint64_t at = v * p.dim + c;
-            if (p.grad_fp32) {
-                float *out = static_cast<float *>(p.grad) + at;
-                *out = p.accumulate ? *out + g : (any ? g : 0.f);
-            } else {
-                __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.grad) + at;
-                *out = __float2bfloat16_rn(p.accumulate ? __bfloat162float(*out) + g : (any ? g : 0.f));
+        } else {
+            put_row<OUT, VEC>(p.grad, (uint64_t)cur * p.dim + col, acc, p.scale, p.accumulate != 0u);
+        }
+    };
+    for (uint32_t i = 0; i < n; i += U) {
+        uint32_t key[U];
+        Pack<DY, VEC> v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            key[u] = i + u < n ? __ldg(p.keys + i0 + i + u) : 0xFFFFFFFFu;
+            if (key[u] < p.rows)
+                v[u] = *reinterpret_cast<const Pack<DY, VEC> *>(static_cast<const DY *>(p.dy) +
+                                                               (uint64_t)__ldg(p.pos + i0 + i + u) * p.ld_dy + col);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (i + u >= n) break;
+            if (key[u] != cur) {
+                if (i + u) {
+                    flush(false);
+                    first = false;
+                }
+                cur = key[u];
+#pragma unroll
+                for (int k = 0; k < VEC; ++k) acc[k] = 0.f;
+            }
+            if (cur < p.rows) {
+#pragma unroll
+                for (int k = 0; k < VEC; ++k) acc[k] += as_float<DY>(v[u].v[k]);
             }
         }
     }
+    flush(true);
+}
+
+// One CTA per (window, 32 columns) whose last row begins in that window and
+// goes on in the next: it adds that row's partial sums, eight threads to a
+// column, each every eighth window, then their eight sums in order.
+template <typename OUT>
+__global__ void __launch_bounds__(256) grad_join(const ReduceParams p) {
+    __shared__ float s_sum[8][33];
+    const uint32_t w = blockIdx.x / p.col_blocks, col = blockIdx.x % p.col_blocks * 32u + (threadIdx.x & 31u);
+    const uint32_t i0 = w * p.window, end = i0 + p.window, sub = threadIdx.x >> 5;
+    if (end >= p.tokens) return;
+    const uint32_t key = __ldg(p.keys + end);
+    if (key >= p.rows || __ldg(p.keys + end - 1u) != key) return;
+    if (__ldg(p.keys + i0) == key && i0 && __ldg(p.keys + i0 - 1u) == key) return;  // it began earlier
+    uint32_t lo = end, hi = p.tokens;  // the first token behind the row's
+    while (lo < hi) {
+        const uint32_t mid = (lo + hi) >> 1;
+        if (__ldg(p.keys + mid) <= key) lo = mid + 1u;
+        else hi = mid;
+    }
+    const uint32_t last = (lo - 1u) / p.window;
+    float sum = 0.f;
+    if (col < p.dim)
+        for (uint32_t k = w + sub; k <= last; k += 8u)
+            sum += p.partial[((uint64_t)k * 2u + (k == w ? 1u : 0u)) * p.dim + col];
+    s_sum[sub][threadIdx.x & 31u] = sum;
+    __syncthreads();
+    if (sub || col >= p.dim) return;
+    for (uint32_t k = 1; k < 8u; ++k) sum += s_sum[k][threadIdx.x];
+    const float acc[1] = {sum};
+    put_row<OUT, 1>(p.grad, (uint64_t)key * p.dim + col, acc, p.scale, p.accumulate != 0u);
 }
 
 dfw_status ids_checked(const void *d_ids, int ids64, uint64_t tokens, uint64_t rows, IdSource &s) {
@@ -305,13 +565,68 @@ dfw_status launch_embed_lanes(const dfw_lanes_scope *scope, uint64_t first, uint
     return cudaGetLastError() == cudaSuccess ? DFW_OK : DFW_ECUDA;
 }
 
-uint64_t embed_grad_scratch(uint64_t tokens, uint32_t) { return tokens ? 16u : 0u; }
+// How the gradient of `tokens` tokens is cut: blocks of `block` tokens for
+// sorting (one if a CTA can hold them all), windows for summing.
+struct GradCut {
+    uint32_t ipt, block, blocks, window, windows;
+    uint64_t list;  // bytes of one array of keys or positions
+};
+
+GradCut grad_cut(uint64_t tokens) {
+    GradCut c;
+    c.ipt = tokens <= 1024u ? 1u : tokens <= 4096u ? 4u : 16u;
+    c.block = SORT_THREADS * c.ipt;
+    c.blocks = (uint32_t)((tokens + c.block - 1u) / c.block);
+    c.window = tokens <= (1u << 14) ? 32u : tokens <= (1u << 17) ? 64u : 128u;
+    c.windows = (uint32_t)((tokens + c.window - 1u) / c.window);
+    c.list = (tokens * 4u + 15u) & ~15ull;
+    return c;
+}
+
+uint64_t embed_grad_scratch(uint64_t tokens, uint32_t dim) {
+    const GradCut c = grad_cut(tokens);
+    return c.list * (c.blocks > 1u ? 4u : 2u) + (c.windows > 1u ? (uint64_t)c.windows * 2u * dim * 4u : 0u);
+}
+
+template <int IPT>
+dfw_status launch_grad_sort(const SortParams &p, unsigned grid, cudaStream_t s) {
+    static int opted[16];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 16) return DFW_ECUDA;
+    if (!opted[dev]) {
+        if (cudaFuncSetAttribute(grad_sort<IPT>, cudaFuncAttributeMaxDynamicSharedMemorySize, sort_smem<IPT>()) != cudaSuccess)
+            return DFW_ECUDA;
+        opted[dev] = 1;
+    }
+    grad_sort<IPT><<<grid, SORT_THREADS, sort_smem<IPT>(), s>>>(p);
+    return cudaGetLastError() == cudaSuccess ? DFW_OK : DFW_ECUDA;
+}
+
+template <typename DY, typename OUT>
+dfw_status launch_grad_reduce(ReduceParams p, bool vec, cudaStream_t s) {
+    constexpr uint32_t V = 16 / sizeof(DY);
+    const uint32_t threads = vec ? p.dim / V : p.dim;
+    p.tpr = 1u;
+    while (p.tpr < 128u && p.tpr < threads) p.tpr *= 2u;
+    p.col_blocks = (threads + p.tpr - 1u) / p.tpr;
+    const uint64_t per = 128u / p.tpr, grid = (p.windows + per - 1u) / per * p.col_blocks;
+    if (grid > 0x7FFFFFFFull) return DFW_EINVAL;
+    if (vec) grad_reduce<DY, OUT, (int)V><<<(unsigned)grid, 128, 0, s>>>(p);
+    else grad_reduce<DY, OUT, 1><<<(unsigned)grid, 128, 0, s>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return DFW_ECUDA;
+    if (p.windows < 2u) return DFW_OK;
+    p.col_blocks = (p.dim + 31u) / 32u;
+    const uint64_t joins = (uint64_t)(p.windows - 1u) * p.col_blocks;
+    if (joins > 0x7FFFFFFFull) return DFW_EINVAL;
+    grad_join<OUT><<<(unsigned)joins, 256, 0, s>>>(p);
+    return cudaGetLastError() == cudaSuccess ? DFW_OK : DFW_ECUDA;
+}
 
 dfw_status launch_embed_grad(const void *d_ids, int ids64, uint64_t tokens, const void *d_dy, int dy_fp32,
                              uint64_t ld_dy, uint64_t rows, uint32_t dim, float scale, void *d_grad, int grad_fp32,
                              int accumulate, void *d_scratch, uint64_t scratch_bytes, cudaStream_t s) {
-    GradParams p;
-    dfw_status st = ids_checked(d_ids, ids64, tokens, rows, p.ids);
+    SortParams sp;
+    dfw_status st = ids_checked(d_ids, ids64, tokens, rows, sp.ids);
     if (st != DFW_OK) return st;
     if (dim < 1u || dim > DFW_EMBED_MAX_DIM || !d_grad || (tokens && (!d_dy || !d_scratch)) || (tokens > 1u && ld_dy < dim) ||
         (dy_fp32 | grad_fp32 | accumulate) & ~1)
@@ -323,17 +638,50 @@ dfw_status launch_embed_grad(const void *d_ids, int ids64, uint64_t tokens, cons
     if (tokens == 0u && accumulate) return DFW_OK;
     int sms = 0;
     if ((st = device_sms(sms)) != DFW_OK) return st;
+    const GradCut cut = grad_cut(tokens);
+    uint8_t *const scratch = static_cast<uint8_t *>(d_scratch);
+    uint32_t *lists[4];
+    for (int i = 0; i < 4; ++i) lists[i] = reinterpret_cast<uint32_t *>(scratch + i * cut.list);
+    // sort the blocks; the other SMs zero the gradient meanwhile
+    sp.keys = lists[0];
+    sp.pos = lists[1];
+    sp.blocks = cut.blocks;
+    sp.passes = 1u;
+    while (rows >> (8u * sp.passes)) ++sp.passes;  // keys go up to `rows`
+    sp.fill = accumulate ? nullptr : static_cast<uint8_t *>(d_grad);
+    sp.fill_bytes = accumulate ? 0u : rows * dim * (grad_fp32 ? 4u : 2u);
+    const uint64_t fillers = sp.fill_bytes ? std::min<uint64_t>((sp.fill_bytes + (1u << 15) - 1u) >> 15, (uint64_t)sms) : 0u;
+    const unsigned grid = (unsigned)(cut.blocks + fillers);
+    st = cut.ipt == 1u ? launch_grad_sort<1>(sp, grid, s) : cut.ipt == 4u ? launch_grad_sort<4>(sp, grid, s) : launch_grad_sort<16>(sp, grid, s);
+    if (st != DFW_OK || tokens == 0u) return st;
+    ReduceParams p;
+    p.keys = lists[0];
+    p.pos = lists[1];
+    if (cut.blocks > 1u) {
+        MergeParams m = {lists[0], lists[1], lists[2], lists[3], (uint32_t)tokens, cut.blocks, cut.block};
+        const auto blocks = [&](uint64_t lanes) { return (unsigned)((tokens * lanes + 255u) / 256u); };
+        if (cut.blocks <= 4u) grad_merge<4><<<blocks(4), 256, 0, s>>>(m);
+        else grad_merge<16><<<blocks(16), 256, 0, s>>>(m);
+        if (cudaGetLastError() != cudaSuccess) return DFW_ECUDA;
+        p.keys = lists[2];
+        p.pos = lists[3];
+    }
     p.dy = d_dy;
     p.grad = d_grad;
+    p.partial = reinterpret_cast<float *>(scratch + (cut.blocks > 1u ? 4u : 2u) * cut.list);
     p.ld_dy = ld_dy;
+    p.tokens = (uint32_t)tokens;
+    p.windows = cut.windows;
+    p.window = cut.window;
     p.dim = dim;
-    p.dy_fp32 = (uint32_t)dy_fp32;
-    p.grad_fp32 = (uint32_t)grad_fp32;
+    p.rows = (uint32_t)rows;
     p.accumulate = (uint32_t)accumulate;
     p.scale = scale;
-    const uint64_t cap = (uint64_t)sms * 8u;
-    embed_grad_scan<<<(unsigned)(rows < cap ? rows : cap), 256, 0, s>>>(p);
-    return cudaGetLastError() == cudaSuccess ? DFW_OK : DFW_ECUDA;
+    // 16-byte loads where every row of dy, and every piece of a gradient row, is aligned for them
+    const bool vec = dim % 8u == 0u && ((reinterpret_cast<uintptr_t>(d_dy) | reinterpret_cast<uintptr_t>(d_grad)) & 15u) == 0u &&
+                     (tokens == 1u || ld_dy * (dy_fp32 ? 4u : 2u) % 16u == 0u);
+    if (dy_fp32) return grad_fp32 ? launch_grad_reduce<float, float>(p, vec, s) : launch_grad_reduce<float, __nv_bfloat16>(p, vec, s);
+    return grad_fp32 ? launch_grad_reduce<__nv_bfloat16, float>(p, vec, s) : launch_grad_reduce<__nv_bfloat16, __nv_bfloat16>(p, vec, s);
 }
 
 }  // namespace dfw
