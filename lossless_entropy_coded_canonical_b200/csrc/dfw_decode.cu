@@ -44,6 +44,13 @@ __device__ unsigned int g_check_site;  // checks build: the first range check th
 }
 
 #include "dfw_device.cuh"
+
+namespace dfw {
+namespace {
+int g_sms[16];  // multiprocessors per device, 0 until asked
+}
+}
+
 #include "dfw_lanes.cuh"
 #include "dfw_rans.cuh"
 #include "dfw_q4.cuh"
@@ -352,8 +359,6 @@ Variant g_variants[] = {
     {8, 512, decode_tiles<8, 512>, {0}},   {16, 128, decode_tiles<16, 128>, {0}},
     {16, 256, decode_tiles<16, 256>, {0}},
 };
-
-int g_sms[16];
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 

@@ -179,81 +179,91 @@ __global__ void __launch_bounds__(128) embed_lanes_rows(const RowsOfLanes p) {
 
 // ------------------------------------------------------ the table's gradient
 
-// Sorting.  A CTA sorts a block of up to 1024 IPT tokens by row, stably, in
-// shared memory: 8 bits a pass from the lowest, each warp ranking its own run
-// of tokens (equal digits of 32 tokens found by one match instruction, so no
-// atomics and a fixed order), then one scan over (digit, warp).  Tokens
-// without a row get key `rows` and end up behind all others.
+// Sorting.  A cluster of C CTAs sorts a block of up to 1024 C IPT tokens by
+// row, stably: 8 bits a pass from the lowest.  Each warp ranks its own run of
+// tokens (equal digits of 32 tokens found by eight ballots: no atomics, a
+// fixed order); each CTA puts its tokens in digit order in its own shared
+// memory, and from there, with the other CTAs' digit counts read through
+// distributed shared memory, in their places in the cluster's order: the
+// remote writes of neighbouring lanes are then neighbours too (writing every
+// token straight to its place measured 4 times as long at 65536 tokens).
+// Tokens without a row get key `rows` and end up behind all others.
 constexpr uint32_t SORT_THREADS = 1024, SORT_WARPS = 32, SORT_STRIDE = 257;
 
 struct SortParams {
     IdSource ids;
     uint32_t *keys, *pos;  // per block: sorted keys and the tokens they belong to
-    uint32_t blocks, passes;
-    uint8_t *fill;         // zeroed meanwhile by the CTAs past the sorting ones (null: nothing)
-    uint64_t fill_bytes;
+    uint32_t *joins;       // the two counters of JoinLists, cleared here
+    uint32_t passes;
 };
 
-template <int IPT>
+template <int C, int IPT>
 constexpr uint32_t sort_smem() {
-    return SORT_WARPS * SORT_STRIDE * 4u + 32u * 4u + SORT_THREADS * IPT * 6u;
+    return SORT_WARPS * SORT_STRIDE * 4u + (256u + 256u + 32u) * 4u + SORT_THREADS * IPT * 8u * (C > 1 ? 2u : 1u);
 }
 
-// Zeroes bytes [0, n) of p from the CTAs [first, gridDim.x).
-__device__ __forceinline__ void zero_fill(uint8_t *p, uint64_t n, uint32_t first) {
-    const uint64_t me = (uint64_t)(blockIdx.x - first) * blockDim.x + threadIdx.x;
-    const uint64_t all = (uint64_t)(gridDim.x - first) * blockDim.x;
-    const uint64_t head = min(n, (uint64_t)(-reinterpret_cast<uintptr_t>(p) & 31u));
-    const uint64_t body = (n - head) >> 5, tail = n - head - (body << 5);
-    if (me < head) p[me] = 0;
-    if (me < tail) p[n - 1u - me] = 0;
-    const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-    for (uint64_t i = me; i < body; i += all) stg256_cs(p + head + (i << 5), z, z);
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The address of this CTA's shared word `a` in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t map_rank(uint32_t a, uint32_t rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ uint32_t ld_cluster(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ void st_cluster(uint32_t a, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
 }
 
-template <int IPT>
+template <int C, int IPT>
 __global__ void __launch_bounds__(SORT_THREADS, 1) grad_sort(const SortParams p) {
-    if (blockIdx.x >= p.blocks) {
-        zero_fill(p.fill, p.fill_bytes, p.blocks);
-        return;
-    }
+    constexpr uint32_t CAP = SORT_THREADS * IPT;
     extern __shared__ __align__(16) uint8_t smem[];
     uint32_t *cnt = reinterpret_cast<uint32_t *>(smem);  // [warp][digit], rows of SORT_STRIDE: a scan's reads hit 32 banks
-    uint32_t *sums = cnt + SORT_WARPS * SORT_STRIDE;
-    uint32_t *s_key = sums + 32;
-    uint16_t *s_pos = reinterpret_cast<uint16_t *>(s_key + SORT_THREADS * IPT);
+    uint32_t *total = cnt + SORT_WARPS * SORT_STRIDE;    // this CTA's count of each digit
+    uint32_t *shift_by = total + 256;                    // from a digit's place in this CTA's order to the cluster's
+    uint32_t *sums = shift_by + 256;
+    uint32_t *s_key = sums + 32, *s_pos = s_key + CAP;            // this CTA's part of the order
+    uint32_t *l_key = C > 1 ? s_pos + CAP : s_key, *l_pos = l_key + CAP;  // this CTA's tokens in digit order
     const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
-    const uint32_t base = blockIdx.x * SORT_THREADS * IPT, run = warp * 32u * IPT + lane;
-    uint32_t key[IPT];
-    uint16_t pos[IPT];
+    const uint32_t rank = blockIdx.x % C, base = blockIdx.x * CAP, run = warp * 32u * IPT + lane;
+    griddep_launch_dependents();
+    if (blockIdx.x == 0u && tid < 2u) p.joins[tid] = 0u;
+    uint32_t key[IPT], pos[IPT];
 #pragma unroll
     for (int j = 0; j < IPT; ++j) {
-        const uint32_t t = base + run + 32u * j;
         uint64_t row = p.ids.rows;
-        pos[j] = (uint16_t)(run + 32u * j);
-        key[j] = 0xFFFFFFFFu;
-        if (t < p.ids.tokens) key[j] = token_row(p.ids, t, row, true) ? (uint32_t)row : (uint32_t)p.ids.rows;
+        pos[j] = base + run + 32u * j;
+        key[j] = 0xFFFFFFFFu;  // behind every token
+        if (pos[j] < p.ids.tokens) key[j] = token_row(p.ids, pos[j], row, true) ? (uint32_t)row : (uint32_t)p.ids.rows;
     }
     for (uint32_t pass = 0; pass < p.passes; ++pass) {
         const uint32_t shift = 8u * pass;
         for (uint32_t i = lane; i < 256u; i += 32u) cnt[warp * SORT_STRIDE + i] = 0u;
         __syncwarp();
-        uint16_t rank[IPT];
+        uint32_t at[IPT];
 #pragma unroll
         for (int j = 0; j < IPT; ++j) {
             const uint32_t d = (key[j] >> shift) & 255u;
-            const uint32_t same = __match_any_sync(0xFFFFFFFFu, d), leader = __ffs(same) - 1u;
-            uint32_t *c = cnt + warp * SORT_STRIDE + d;
-            uint32_t old = 0;
-            if (lane == leader) {
-                old = *c;
-                *c = old + __popc(same);
+            uint32_t same = 0xFFFFFFFFu;
+#pragma unroll
+            for (int b = 0; b < 8; ++b) {
+                const uint32_t v = __ballot_sync(0xFFFFFFFFu, (d >> b) & 1u);
+                same &= (d >> b) & 1u ? v : ~v;
             }
-            rank[j] = (uint16_t)(__shfl_sync(0xFFFFFFFFu, old, leader) + __popc(same & ((1u << lane) - 1u)));
+            uint32_t *c = cnt + warp * SORT_STRIDE + d;
+            at[j] = *c + __popc(same & ((1u << lane) - 1u));
+            __syncwarp();
+            if (lane == __ffs(same) - 1u) *c += __popc(same);
             __syncwarp();
         }
         __syncthreads();
-        // exclusive offsets in (digit, warp) order: thread i takes digit i / 4, warps 8 (i mod 4) .. + 7
+        // offsets in (digit, warp) order: thread i takes digit i / 4, warps 8 (i mod 4) .. + 7
         uint32_t *mine = cnt + 8u * (tid & 3u) * SORT_STRIDE + (tid >> 2), sum = 0;
 #pragma unroll
         for (uint32_t k = 0; k < 8u; ++k) {
@@ -261,46 +271,99 @@ __global__ void __launch_bounds__(SORT_THREADS, 1) grad_sort(const SortParams p)
             mine[k * SORT_STRIDE] = sum;
             sum += v;
         }
-        uint32_t incl = sum;
+        uint32_t four = sum;  // prefix over the digit's four threads
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, incl, d);
-            if (lane >= (uint32_t)d) incl += y;
+        for (uint32_t d = 1; d < 4u; d <<= 1) {
+            const uint32_t z = __shfl_up_sync(0xFFFFFFFFu, four, d);
+            if ((tid & 3u) >= d) four += z;
         }
-        if (lane == 31u) sums[warp] = incl;
-        __syncthreads();
-        uint32_t before = sums[lane];
+        const uint32_t all4 = __shfl_sync(0xFFFFFFFFu, four, lane | 3u), warps_before = four - sum;
+        // exclusive prefix over the digits of v, which every fourth thread holds for its digit
+        auto before_digit = [&](uint32_t v) {
+            uint32_t incl = v;
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, before, d);
-            if (lane >= (uint32_t)d) before += y;
-        }
-        before = __shfl_sync(0xFFFFFFFFu, before, (warp + 31u) & 31u);
-        const uint32_t off = (warp ? before : 0u) + incl - sum;
+            for (int d = 4; d < 32; d <<= 1) {
+                const uint32_t z = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+                if (lane >= (uint32_t)d) incl += z;
+            }
+            __syncthreads();  // sums may still be read from the last call
+            if (lane == 31u) sums[warp] = incl;
+            __syncthreads();
+            uint32_t w = sums[lane];
 #pragma unroll
-        for (uint32_t k = 0; k < 8u; ++k) mine[k * SORT_STRIDE] += off;
+            for (int d = 1; d < 32; d <<= 1) {
+                const uint32_t z = __shfl_up_sync(0xFFFFFFFFu, w, d);
+                if (lane >= (uint32_t)d) w += z;
+            }
+            w = __shfl_sync(0xFFFFFFFFu, w, (warp + 31u) & 31u);
+            return (warp ? w : 0u) + incl - v;
+        };
+        const uint32_t here = before_digit(all4);
+#pragma unroll
+        for (uint32_t k = 0; k < 8u; ++k) mine[k * SORT_STRIDE] += here + warps_before;
+        if (C > 1 && !(tid & 3u)) total[tid >> 2] = all4;
         __syncthreads();
 #pragma unroll
         for (int j = 0; j < IPT; ++j) {
-            const uint32_t to = cnt[warp * SORT_STRIDE + ((key[j] >> shift) & 255u)] + rank[j];
-            s_key[to] = key[j];
-            s_pos[to] = pos[j];
+            const uint32_t to = cnt[warp * SORT_STRIDE + ((key[j] >> shift) & 255u)] + at[j];
+            l_key[to] = key[j];
+            l_pos[to] = pos[j];
         }
-        __syncthreads();
+        if constexpr (C > 1) {
+            cluster_sync();  // every CTA's counts are out, and its part of the last order has been read
+            uint32_t v[C], everywhere = 0, earlier = 0;
+            const uint32_t a = smem_u32(total + (tid >> 2));
+#pragma unroll
+            for (uint32_t r = 0; r < C; ++r) v[r] = ld_cluster(map_rank(a, r));
+#pragma unroll
+            for (uint32_t r = 0; r < C; ++r) {
+                everywhere += v[r];
+                if (r < rank) earlier += v[r];
+            }
+            const uint32_t there = before_digit(everywhere) + earlier;
+            if (!(tid & 3u)) shift_by[tid >> 2] = there - here;
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < IPT; ++j) {
+                const uint32_t from = run + 32u * j, k = l_key[from];
+                const uint32_t to = from + shift_by[(k >> shift) & 255u], r = to / CAP, i = to % CAP;
+                st_cluster(map_rank(smem_u32(s_key + i), r), k);
+                st_cluster(map_rank(smem_u32(s_pos + i), r), l_pos[from]);
+            }
+            cluster_sync();
+        } else {
+            __syncthreads();
+        }
 #pragma unroll
         for (int j = 0; j < IPT; ++j) {
             key[j] = s_key[run + 32u * j];
             pos[j] = s_pos[run + 32u * j];
         }
+        if constexpr (C == 1) __syncthreads();  // before the next pass writes
     }
 #pragma unroll
     for (int j = 0; j < IPT; ++j) {
         const uint32_t t = base + run + 32u * j;
         if (t < p.ids.tokens) {
             p.keys[t] = key[j];
-            p.pos[t] = base + pos[j];
+            p.pos[t] = pos[j];
         }
     }
+}
+
+// Zeroes the gradient while the tokens are sorted: a programmatic dependent
+// of the sort that starts beside it, and ends after it (so that what follows
+// on the stream follows both).
+__global__ void __launch_bounds__(512) grad_zero(uint8_t *p, uint64_t n) {
+    griddep_launch_dependents();
+    const uint64_t me = (uint64_t)blockIdx.x * blockDim.x + threadIdx.x, all = (uint64_t)gridDim.x * blockDim.x;
+    const uint64_t head = min(n, (uint64_t)(-reinterpret_cast<uintptr_t>(p) & 31u));
+    const uint64_t body = (n - head) >> 5, tail = n - head - (body << 5);
+    if (me < head) p[me] = 0;
+    if (me < tail) p[n - 1u - me] = 0;
+    const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+    for (uint64_t i = me; i < body; i += all) stg256_cs(p + head + (i << 5), z, z);
+    griddep_wait();
 }
 
 // Joins sorted blocks into one order: a token's place is its place in its own
@@ -315,6 +378,7 @@ struct MergeParams {
 
 template <int LANES>
 __global__ void __launch_bounds__(256) grad_merge(const MergeParams p) {
+    griddep_launch_dependents();
     const uint64_t i = (blockIdx.x * 256ull + threadIdx.x) / LANES;
     const uint32_t sub = threadIdx.x % LANES;
     const uint32_t t = (uint32_t)min(i, (uint64_t)p.tokens - 1u);
@@ -343,6 +407,13 @@ __global__ void __launch_bounds__(256) grad_merge(const MergeParams p) {
     }
 }
 
+// Rows that begin in a window and go on in the next, for grad_join: joins[0]
+// and joins[1] count two lists of such windows, those whose row ends within
+// JOIN_FEW more windows (window | further windows << 24, at joins + 4) and the
+// rest (at joins + 4 + windows).  Their order does not matter: each is joined
+// by itself.
+constexpr uint32_t JOIN_FEW = 8;
+
 // Summing.  The sorted tokens are cut into windows of `window`; a thread
 // walks a window with VEC columns, eight rows of dy in flight, and writes a
 // row's sum when the next row's tokens begin.  A row whose tokens reach past
@@ -353,6 +424,7 @@ struct ReduceParams {
     const void *dy;
     void *grad;
     float *partial;  // [windows][2][dim]
+    uint32_t *joins;
     uint64_t ld_dy;
     uint32_t tokens, windows, window, dim, rows;
     uint32_t tpr;          // threads per window (a power of two)
@@ -379,6 +451,29 @@ struct __align__(sizeof(T) * N) Pack {
     T v[N];
 };
 
+// VEC values of a row of dy as they are in memory: whole words, so that the
+// rows in flight take no more registers than bytes.
+template <typename T, int VEC>
+struct Raw;
+template <int VEC>
+struct Raw<float, VEC> {
+    Pack<float, VEC> p;
+    __device__ __forceinline__ float get(int k) const { return p.v[k]; }
+};
+template <>
+struct Raw<__nv_bfloat16, 1> {
+    uint16_t p;
+    __device__ __forceinline__ float get(int) const { return __uint_as_float((uint32_t)p << 16); }
+};
+template <>
+struct Raw<__nv_bfloat16, 8> {
+    uint4 p;
+    __device__ __forceinline__ float get(int k) const {
+        const uint32_t w = k < 2 ? p.x : k < 4 ? p.y : k < 6 ? p.z : p.w;
+        return __uint_as_float(k & 1 ? w & 0xFFFF0000u : w << 16);
+    }
+};
+
 // Writes (or adds) scale x sum to VEC columns of a row, rounded once.
 template <typename OUT, int VEC>
 __device__ __forceinline__ void put_row(void *grad, uint64_t at, const float (&acc)[VEC], float scale, bool add) {
@@ -395,18 +490,47 @@ __device__ __forceinline__ void put_row(void *grad, uint64_t at, const float (&a
 }
 
 template <typename DY, typename OUT, int VEC>
-__global__ void __launch_bounds__(128) grad_reduce(const ReduceParams p) {
+__global__ void __launch_bounds__(128, 6) grad_reduce(const ReduceParams p) {
     constexpr int U = 8;  // rows in flight
-    const uint32_t per = 128u / p.tpr;  // windows a CTA walks at once
-    const uint32_t w = blockIdx.x / p.col_blocks * per + threadIdx.x / p.tpr;
+    griddep_launch_dependents();
+    griddep_wait();
+    extern __shared__ uint32_t s_list[];  // keys, then positions, of the CTA's windows
+    const uint32_t per = 128u / p.tpr;    // windows a CTA walks at once
+    const uint32_t w0 = blockIdx.x / p.col_blocks * per, list = per * p.window;
+    for (uint32_t i = threadIdx.x; i < list; i += 128u) {
+        const uint64_t t = (uint64_t)w0 * p.window + i;
+        const bool in = t < p.tokens;
+        s_list[i] = in ? __ldg(p.keys + t) : 0xFFFFFFFFu;
+        s_list[list + i] = in ? __ldg(p.pos + t) : 0u;
+    }
+    const uint32_t w = w0 + threadIdx.x / p.tpr;
     const uint32_t col = (blockIdx.x % p.col_blocks * p.tpr + threadIdx.x % p.tpr) * VEC;
-    if (w >= p.windows || col >= p.dim) return;
-    const uint32_t i0 = w * p.window, n = min(p.window, p.tokens - i0);
-    const uint32_t prev = i0 ? __ldg(p.keys + i0 - 1u) : 0xFFFFFFFFu;
-    const uint32_t next = i0 + n < p.tokens ? __ldg(p.keys + i0 + n) : 0xFFFFFFFFu;
+    const bool live = w < p.windows && col < p.dim;
+    const uint32_t i0 = w * p.window, n = live ? min(p.window, p.tokens - i0) : 0u;
+    const uint32_t prev = live && i0 ? __ldg(p.keys + i0 - 1u) : 0xFFFFFFFFu;
+    const uint32_t next = live && i0 + n < p.tokens ? __ldg(p.keys + i0 + n) : 0xFFFFFFFFu;
+    __syncthreads();
+    if (!live) return;
+    const uint32_t *keys = s_list + threadIdx.x / p.tpr * p.window, *pos = keys + list;
+    if (col == 0u && n == p.window) {
+        const uint32_t tail = keys[n - 1u];
+        if (tail < p.rows && tail == next && !(keys[0] == tail && prev == tail)) {
+            uint32_t more = 1u;  // windows after this one that begin with the row
+            bool on = true;
+#pragma unroll
+            for (uint32_t k = 2; k <= JOIN_FEW; ++k) {
+                const uint64_t t = (uint64_t)(w + k) * p.window;
+                on = on && t < p.tokens && __ldg(p.keys + min(t, (uint64_t)p.tokens - 1u)) == tail;
+                more += on;
+            }
+            if (more < JOIN_FEW) p.joins[4u + atomicAdd(p.joins, 1u)] = w | more << 24;
+            else p.joins[4u + p.windows + atomicAdd(p.joins + 1, 1u)] = w;
+        }
+    }
+    const DY *dy = static_cast<const DY *>(p.dy) + col;
     float acc[VEC];
     uint32_t cur = 0xFFFFFFFFu;  // the row being summed
-    bool first = true;           // its tokens began before the window, or at its first token
+    bool first = true;           // it is the window's first
     auto flush = [&](bool last) {
         if (cur >= p.rows) return;
         const bool left = first && cur == prev, right = last && cur == next;
@@ -424,66 +548,85 @@ __global__ void __launch_bounds__(128) grad_reduce(const ReduceParams p) {
             put_row<OUT, VEC>(p.grad, (uint64_t)cur * p.dim + col, acc, p.scale, p.accumulate != 0u);
         }
     };
-    for (uint32_t i = 0; i < n; i += U) {
-        uint32_t key[U];
-        Pack<DY, VEC> v[U];
+    for (uint32_t i = 0; i < n; i += U) {  // window is a multiple of U: keys past the last token read as no row
+        Raw<DY, VEC> v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (keys[i + u] < p.rows) v[u] = *reinterpret_cast<const Raw<DY, VEC> *>(dy + (uint64_t)pos[i + u] * p.ld_dy);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            key[u] = i + u < n ? __ldg(p.keys + i0 + i + u) : 0xFFFFFFFFu;
-            if (key[u] < p.rows)
-                v[u] = *reinterpret_cast<const Pack<DY, VEC> *>(static_cast<const DY *>(p.dy) +
-                                                               (uint64_t)__ldg(p.pos + i0 + i + u) * p.ld_dy + col);
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (i + u >= n) break;
-            if (key[u] != cur) {
+            const uint32_t key = keys[i + u];
+            if (key != cur) {
                 if (i + u) {
                     flush(false);
                     first = false;
                 }
-                cur = key[u];
+                cur = key;
 #pragma unroll
                 for (int k = 0; k < VEC; ++k) acc[k] = 0.f;
             }
             if (cur < p.rows) {
 #pragma unroll
-                for (int k = 0; k < VEC; ++k) acc[k] += as_float<DY>(v[u].v[k]);
+                for (int k = 0; k < VEC; ++k) acc[k] += v[u].get(k);
             }
         }
     }
     flush(true);
 }
 
-// One CTA per (window, 32 columns) whose last row begins in that window and
-// goes on in the next: it adds that row's partial sums, eight threads to a
-// column, each every eighth window, then their eight sums in order.
-template <typename OUT>
+// Adds the partial sums of the listed rows.  Few windows: a thread adds all
+// of them for its VEC columns.  Many (a row that a good part of the tokens
+// share): for 32 VEC columns at a time each warp adds every eighth window,
+// then the eight sums are added in order.
+template <typename OUT, int VEC>
 __global__ void __launch_bounds__(256) grad_join(const ReduceParams p) {
-    __shared__ float s_sum[8][33];
-    const uint32_t w = blockIdx.x / p.col_blocks, col = blockIdx.x % p.col_blocks * 32u + (threadIdx.x & 31u);
-    const uint32_t i0 = w * p.window, end = i0 + p.window, sub = threadIdx.x >> 5;
-    if (end >= p.tokens) return;
-    const uint32_t key = __ldg(p.keys + end);
-    if (key >= p.rows || __ldg(p.keys + end - 1u) != key) return;
-    if (__ldg(p.keys + i0) == key && i0 && __ldg(p.keys + i0 - 1u) == key) return;  // it began earlier
-    uint32_t lo = end, hi = p.tokens;  // the first token behind the row's
-    while (lo < hi) {
-        const uint32_t mid = (lo + hi) >> 1;
-        if (__ldg(p.keys + mid) <= key) lo = mid + 1u;
-        else hi = mid;
+    __shared__ float s_sum[8][32 * VEC];
+    griddep_wait();
+    const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
+    const uint32_t few = *reinterpret_cast<volatile uint32_t *>(p.joins), many = *reinterpret_cast<volatile uint32_t *>(p.joins + 1);
+    const uint32_t narrow = (p.dim + 32u * VEC - 1u) / (32u * VEC), wide = (p.dim + 256u * VEC - 1u) / (256u * VEC);
+    auto add = [&](float (&sum)[VEC], uint32_t k, uint32_t slot, uint32_t col) {
+        const Pack<float, VEC> v = *reinterpret_cast<const Pack<float, VEC> *>(p.partial + ((uint64_t)k * 2u + slot) * p.dim + col);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) sum[j] += v.v[j];
+    };
+    for (uint64_t item = blockIdx.x; item < (uint64_t)many * narrow; item += gridDim.x) {
+        const uint32_t w = p.joins[4u + p.windows + (uint32_t)(item / narrow)];
+        const uint32_t col = (uint32_t)(item % narrow) * 32u * VEC + lane * VEC, key = __ldg(p.keys + (uint64_t)(w + 1u) * p.window);
+        uint32_t last = w + JOIN_FEW;  // the last window that begins with the row, 32 windows at a look
+        for (;;) {
+            const uint64_t t = (uint64_t)(last + 1u + lane) * p.window;
+            const uint32_t m = __ballot_sync(0xFFFFFFFFu, t < p.tokens && __ldg(p.keys + min(t, (uint64_t)p.tokens - 1u)) == key);
+            last += m == 0xFFFFFFFFu ? 32u : __ffs(~m) - 1u;
+            if (m != 0xFFFFFFFFu) break;
+        }
+        float sum[VEC] = {};
+        if (col < p.dim) {
+#pragma unroll 8
+            for (uint32_t k = w + warp; k <= last; k += 8u) add(sum, k, k == w ? 1u : 0u, col);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) s_sum[warp][lane * VEC + j] = sum[j];
+        __syncthreads();
+        if (warp || col >= p.dim) continue;
+#pragma unroll
+        for (int j = 0; j < VEC; ++j)
+            for (uint32_t k = 1; k < 8u; ++k) sum[j] += s_sum[k][lane * VEC + j];
+        put_row<OUT, VEC>(p.grad, (uint64_t)key * p.dim + col, sum, p.scale, p.accumulate != 0u);
     }
-    const uint32_t last = (lo - 1u) / p.window;
-    float sum = 0.f;
-    if (col < p.dim)
-        for (uint32_t k = w + sub; k <= last; k += 8u)
-            sum += p.partial[((uint64_t)k * 2u + (k == w ? 1u : 0u)) * p.dim + col];
-    s_sum[sub][threadIdx.x & 31u] = sum;
-    __syncthreads();
-    if (sub || col >= p.dim) return;
-    for (uint32_t k = 1; k < 8u; ++k) sum += s_sum[k][threadIdx.x];
-    const float acc[1] = {sum};
-    put_row<OUT, 1>(p.grad, (uint64_t)key * p.dim + col, acc, p.scale, p.accumulate != 0u);
+    for (uint64_t item = blockIdx.x; item < (uint64_t)few * wide; item += gridDim.x) {
+        const uint32_t entry = p.joins[4u + (uint32_t)(item / wide)], w = entry & 0xFFFFFFu, more = entry >> 24;
+        const uint32_t col = ((uint32_t)(item % wide) * 256u + threadIdx.x) * VEC;
+        if (col >= p.dim) continue;
+        const uint32_t key = __ldg(p.keys + (uint64_t)(w + 1u) * p.window);
+        float sum[VEC] = {};
+        add(sum, w, 1u, col);
+#pragma unroll
+        for (uint32_t k = 1; k < JOIN_FEW; ++k)
+            if (k <= more) add(sum, w + k, 0u, col);
+        put_row<OUT, VEC>(p.grad, (uint64_t)key * p.dim + col, sum, p.scale, p.accumulate != 0u);
+    }
 }
 
 dfw_status ids_checked(const void *d_ids, int ids64, uint64_t tokens, uint64_t rows, IdSource &s) {
@@ -565,61 +708,86 @@ dfw_status launch_embed_lanes(const dfw_lanes_scope *scope, uint64_t first, uint
     return cudaGetLastError() == cudaSuccess ? DFW_OK : DFW_ECUDA;
 }
 
-// How the gradient of `tokens` tokens is cut: blocks of `block` tokens for
-// sorting (one if a CTA can hold them all), windows for summing.
+// How the gradient of `tokens` tokens is cut: blocks of `block` tokens that a
+// cluster sorts, windows for summing.
 struct GradCut {
-    uint32_t ipt, block, blocks, window, windows;
-    uint64_t list;  // bytes of one array of keys or positions
+    uint32_t ctas, ipt, block, blocks, window, windows;
+    uint32_t joins;  // bytes of the joins lists
+    uint64_t list;   // bytes of one array of keys or positions
 };
 
 GradCut grad_cut(uint64_t tokens) {
     GradCut c;
-    c.ipt = tokens <= 1024u ? 1u : tokens <= 4096u ? 4u : 16u;
-    c.block = SORT_THREADS * c.ipt;
+    c.ctas = tokens <= 1024u ? 1u : 8u;
+    c.ipt = tokens <= 8192u ? 1u : tokens <= 32768u ? 4u : 8u;
+    c.block = SORT_THREADS * c.ctas * c.ipt;
     c.blocks = (uint32_t)((tokens + c.block - 1u) / c.block);
-    c.window = tokens <= (1u << 14) ? 32u : tokens <= (1u << 17) ? 64u : 128u;
+    c.window = tokens <= 1024u ? 8u : tokens <= (1u << 14) ? 32u : tokens <= (1u << 17) ? 64u : 128u;
     c.windows = (uint32_t)((tokens + c.window - 1u) / c.window);
     c.list = (tokens * 4u + 15u) & ~15ull;
+    c.joins = ((4u + 2u * c.windows) * 4u + 15u) & ~15u;
     return c;
 }
 
 uint64_t embed_grad_scratch(uint64_t tokens, uint32_t dim) {
+    if (tokens == 0u) return 0u;
     const GradCut c = grad_cut(tokens);
-    return c.list * (c.blocks > 1u ? 4u : 2u) + (c.windows > 1u ? (uint64_t)c.windows * 2u * dim * 4u : 0u);
+    return c.joins + c.list * (c.blocks > 1u ? 4u : 2u) + (c.windows > 1u ? (uint64_t)c.windows * 2u * dim * 4u : 0u);
 }
 
-template <int IPT>
-dfw_status launch_grad_sort(const SortParams &p, unsigned grid, cudaStream_t s) {
+// A launch that may be a programmatic dependent of the one before (the kernel
+// then waits for that itself) or run in clusters.
+template <typename F, typename... A>
+dfw_status launch_with(F fn, uint64_t grid, unsigned block, uint32_t smem, bool dependent, unsigned cluster, cudaStream_t s,
+                       A... args) {
+    if (grid > 0x7FFFFFFFull) return DFW_EINVAL;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    cfg.attrs = attr;
+    cfg.numAttrs = 0;
+    if (dependent) {
+        attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (cluster > 1u) {
+        attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+        attr[cfg.numAttrs].val.clusterDim.x = cluster;
+        attr[cfg.numAttrs].val.clusterDim.y = 1;
+        attr[cfg.numAttrs++].val.clusterDim.z = 1;
+    }
+    return cudaLaunchKernelEx(&cfg, fn, args...) == cudaSuccess ? DFW_OK : DFW_ECUDA;
+}
+
+template <int C, int IPT>
+dfw_status launch_grad_sort(const SortParams &p, uint32_t blocks, cudaStream_t s) {
     static int opted[16];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 16) return DFW_ECUDA;
     if (!opted[dev]) {
-        if (cudaFuncSetAttribute(grad_sort<IPT>, cudaFuncAttributeMaxDynamicSharedMemorySize, sort_smem<IPT>()) != cudaSuccess)
+        if (cudaFuncSetAttribute(grad_sort<C, IPT>, cudaFuncAttributeMaxDynamicSharedMemorySize, sort_smem<C, IPT>()) != cudaSuccess)
             return DFW_ECUDA;
         opted[dev] = 1;
     }
-    grad_sort<IPT><<<grid, SORT_THREADS, sort_smem<IPT>(), s>>>(p);
-    return cudaGetLastError() == cudaSuccess ? DFW_OK : DFW_ECUDA;
+    return launch_with(grad_sort<C, IPT>, blocks * C, SORT_THREADS, sort_smem<C, IPT>(), false, C, s, p);
 }
 
-template <typename DY, typename OUT>
-dfw_status launch_grad_reduce(ReduceParams p, bool vec, cudaStream_t s) {
-    constexpr uint32_t V = 16 / sizeof(DY);
-    const uint32_t threads = vec ? p.dim / V : p.dim;
-    p.tpr = 1u;
+template <typename DY, typename OUT, int V>
+dfw_status launch_grad_reduce(ReduceParams p, int sms, cudaStream_t s) {
+    const uint32_t threads = (p.dim + V - 1u) / V;
+    p.tpr = 8u;
     while (p.tpr < 128u && p.tpr < threads) p.tpr *= 2u;
     p.col_blocks = (threads + p.tpr - 1u) / p.tpr;
-    const uint64_t per = 128u / p.tpr, grid = (p.windows + per - 1u) / per * p.col_blocks;
-    if (grid > 0x7FFFFFFFull) return DFW_EINVAL;
-    if (vec) grad_reduce<DY, OUT, (int)V><<<(unsigned)grid, 128, 0, s>>>(p);
-    else grad_reduce<DY, OUT, 1><<<(unsigned)grid, 128, 0, s>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return DFW_ECUDA;
-    if (p.windows < 2u) return DFW_OK;
-    p.col_blocks = (p.dim + 31u) / 32u;
-    const uint64_t joins = (uint64_t)(p.windows - 1u) * p.col_blocks;
-    if (joins > 0x7FFFFFFFull) return DFW_EINVAL;
-    grad_join<OUT><<<(unsigned)joins, 256, 0, s>>>(p);
-    return cudaGetLastError() == cudaSuccess ? DFW_OK : DFW_ECUDA;
+    const uint64_t per = 128u / p.tpr;
+    dfw_status st = launch_with(grad_reduce<DY, OUT, V>, (p.windows + per - 1u) / per * p.col_blocks, 128, per * p.window * 8u,
+                                true, 1, s, p);
+    if (st != DFW_OK || p.windows < 2u) return st;
+    constexpr uint32_t J = V > 4 ? 4 : V;
+    const uint64_t most = (uint64_t)(p.windows - 1u) * ((p.dim + 32u * J - 1u) / (32u * J));
+    return launch_with(grad_join<OUT, (int)J>, std::min<uint64_t>(most, (uint64_t)sms * 8u), 256, 0, true, 1, s, p);
 }
 
 dfw_status launch_embed_grad(const void *d_ids, int ids64, uint64_t tokens, const void *d_dy, int dy_fp32,
@@ -638,37 +806,38 @@ dfw_status launch_embed_grad(const void *d_ids, int ids64, uint64_t tokens, cons
     if (tokens == 0u && accumulate) return DFW_OK;
     int sms = 0;
     if ((st = device_sms(sms)) != DFW_OK) return st;
+    uint8_t *const fill = static_cast<uint8_t *>(d_grad);
+    const uint64_t fill_bytes = accumulate ? 0u : rows * dim * (grad_fp32 ? 4u : 2u);
+    const uint64_t fillers = std::min<uint64_t>((fill_bytes + (1u << 14) - 1u) >> 14, (uint64_t)sms * 4u);
+    if (tokens == 0u) return launch_with(grad_zero, fillers, 512, 0, false, 1, s, fill, fill_bytes);
     const GradCut cut = grad_cut(tokens);
     uint8_t *const scratch = static_cast<uint8_t *>(d_scratch);
     uint32_t *lists[4];
-    for (int i = 0; i < 4; ++i) lists[i] = reinterpret_cast<uint32_t *>(scratch + i * cut.list);
-    // sort the blocks; the other SMs zero the gradient meanwhile
+    for (int i = 0; i < 4; ++i) lists[i] = reinterpret_cast<uint32_t *>(scratch + cut.joins + i * cut.list);
     sp.keys = lists[0];
     sp.pos = lists[1];
-    sp.blocks = cut.blocks;
+    sp.joins = reinterpret_cast<uint32_t *>(scratch);
     sp.passes = 1u;
     while (rows >> (8u * sp.passes)) ++sp.passes;  // keys go up to `rows`
-    sp.fill = accumulate ? nullptr : static_cast<uint8_t *>(d_grad);
-    sp.fill_bytes = accumulate ? 0u : rows * dim * (grad_fp32 ? 4u : 2u);
-    const uint64_t fillers = sp.fill_bytes ? std::min<uint64_t>((sp.fill_bytes + (1u << 15) - 1u) >> 15, (uint64_t)sms) : 0u;
-    const unsigned grid = (unsigned)(cut.blocks + fillers);
-    st = cut.ipt == 1u ? launch_grad_sort<1>(sp, grid, s) : cut.ipt == 4u ? launch_grad_sort<4>(sp, grid, s) : launch_grad_sort<16>(sp, grid, s);
-    if (st != DFW_OK || tokens == 0u) return st;
+    st = cut.ctas == 1u ? launch_grad_sort<1, 1>(sp, cut.blocks, s)
+         : cut.ipt == 1u ? launch_grad_sort<8, 1>(sp, cut.blocks, s)
+         : cut.ipt == 4u ? launch_grad_sort<8, 4>(sp, cut.blocks, s)
+                         : launch_grad_sort<8, 8>(sp, cut.blocks, s);
+    if (st != DFW_OK) return st;
+    if (fill_bytes && (st = launch_with(grad_zero, fillers, 512, 0, true, 1, s, fill, fill_bytes)) != DFW_OK) return st;
     ReduceParams p;
     p.keys = lists[0];
     p.pos = lists[1];
     if (cut.blocks > 1u) {
         MergeParams m = {lists[0], lists[1], lists[2], lists[3], (uint32_t)tokens, cut.blocks, cut.block};
-        const auto blocks = [&](uint64_t lanes) { return (unsigned)((tokens * lanes + 255u) / 256u); };
-        if (cut.blocks <= 4u) grad_merge<4><<<blocks(4), 256, 0, s>>>(m);
-        else grad_merge<16><<<blocks(16), 256, 0, s>>>(m);
-        if (cudaGetLastError() != cudaSuccess) return DFW_ECUDA;
+        if ((st = launch_with(grad_merge<16>, (tokens * 16u + 255u) / 256u, 256, 0, false, 1, s, m)) != DFW_OK) return st;
         p.keys = lists[2];
         p.pos = lists[3];
     }
     p.dy = d_dy;
     p.grad = d_grad;
-    p.partial = reinterpret_cast<float *>(scratch + (cut.blocks > 1u ? 4u : 2u) * cut.list);
+    p.partial = reinterpret_cast<float *>(scratch + cut.joins + (cut.blocks > 1u ? 4u : 2u) * cut.list);
+    p.joins = sp.joins;
     p.ld_dy = ld_dy;
     p.tokens = (uint32_t)tokens;
     p.windows = cut.windows;
@@ -680,8 +849,13 @@ dfw_status launch_embed_grad(const void *d_ids, int ids64, uint64_t tokens, cons
     // 16-byte loads where every row of dy, and every piece of a gradient row, is aligned for them
     const bool vec = dim % 8u == 0u && ((reinterpret_cast<uintptr_t>(d_dy) | reinterpret_cast<uintptr_t>(d_grad)) & 15u) == 0u &&
                      (tokens == 1u || ld_dy * (dy_fp32 ? 4u : 2u) % 16u == 0u);
-    if (dy_fp32) return grad_fp32 ? launch_grad_reduce<float, float>(p, vec, s) : launch_grad_reduce<float, __nv_bfloat16>(p, vec, s);
-    return grad_fp32 ? launch_grad_reduce<__nv_bfloat16, float>(p, vec, s) : launch_grad_reduce<__nv_bfloat16, __nv_bfloat16>(p, vec, s);
+    typedef __nv_bfloat16 bf;
+    if (vec) {
+        if (dy_fp32) return grad_fp32 ? launch_grad_reduce<float, float, 4>(p, sms, s) : launch_grad_reduce<float, bf, 4>(p, sms, s);
+        return grad_fp32 ? launch_grad_reduce<bf, float, 8>(p, sms, s) : launch_grad_reduce<bf, bf, 8>(p, sms, s);
+    }
+    if (dy_fp32) return grad_fp32 ? launch_grad_reduce<float, float, 1>(p, sms, s) : launch_grad_reduce<float, bf, 1>(p, sms, s);
+    return grad_fp32 ? launch_grad_reduce<bf, float, 1>(p, sms, s) : launch_grad_reduce<bf, bf, 1>(p, sms, s);
 }
 
 }  // namespace dfw

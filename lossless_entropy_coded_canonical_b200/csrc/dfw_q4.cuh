@@ -219,12 +219,14 @@ dfw_status q4_checked(const dfw_q4_info *info, const void *d_packed, Q4Params &p
     return reinterpret_cast<uintptr_t>(d_packed) & 15u ? DFW_EALIGN : DFW_OK;
 }
 
+// The current device's multiprocessors (asked once per device).
 dfw_status device_sms(int &sms) {
     int dev = 0;
-    return cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < 16 &&
-                   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess
-               ? DFW_OK
-               : DFW_ECUDA;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 16) return DFW_ECUDA;
+    if (!g_sms[dev] && cudaDeviceGetAttribute(&g_sms[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return DFW_ECUDA;
+    sms = g_sms[dev];
+    return DFW_OK;
 }
 
 unsigned q4_grid(const Q4Params &p, int sms, unsigned per_sm) {
