@@ -202,24 +202,6 @@ constexpr uint32_t sort_smem() {
     return SORT_WARPS * SORT_STRIDE * 4u + (256u + 256u + 32u) * 4u + SORT_THREADS * IPT * 8u * (C > 1 ? 2u : 1u);
 }
 
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// The address of this CTA's shared word `a` in CTA `rank` of the cluster.
-__device__ __forceinline__ uint32_t map_rank(uint32_t a, uint32_t rank) {
-    uint32_t r;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
-    return r;
-}
-__device__ __forceinline__ uint32_t ld_cluster(uint32_t a) {
-    uint32_t v;
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-    return v;
-}
-__device__ __forceinline__ void st_cluster(uint32_t a, uint32_t v) {
-    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
-}
-
 template <int C, int IPT>
 __global__ void __launch_bounds__(SORT_THREADS, 1) grad_sort(const SortParams p) {
     constexpr uint32_t CAP = SORT_THREADS * IPT;
@@ -733,33 +715,6 @@ uint64_t embed_grad_scratch(uint64_t tokens, uint32_t dim) {
     if (tokens == 0u) return 0u;
     const GradCut c = grad_cut(tokens);
     return c.joins + c.list * (c.blocks > 1u ? 4u : 2u) + (c.windows > 1u ? (uint64_t)c.windows * 2u * dim * 4u : 0u);
-}
-
-// A launch that may be a programmatic dependent of the one before (the kernel
-// then waits for that itself) or run in clusters.
-template <typename F, typename... A>
-dfw_status launch_with(F fn, uint64_t grid, unsigned block, uint32_t smem, bool dependent, unsigned cluster, cudaStream_t s,
-                       A... args) {
-    if (grid > 0x7FFFFFFFull) return DFW_EINVAL;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(block);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[2];
-    cfg.attrs = attr;
-    cfg.numAttrs = 0;
-    if (dependent) {
-        attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
-    }
-    if (cluster > 1u) {
-        attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
-        attr[cfg.numAttrs].val.clusterDim.x = cluster;
-        attr[cfg.numAttrs].val.clusterDim.y = 1;
-        attr[cfg.numAttrs++].val.clusterDim.z = 1;
-    }
-    return cudaLaunchKernelEx(&cfg, fn, args...) == cudaSuccess ? DFW_OK : DFW_ECUDA;
 }
 
 template <int C, int IPT>

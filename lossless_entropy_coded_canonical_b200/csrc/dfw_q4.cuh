@@ -23,10 +23,64 @@
 
 #include <cuda_bf16.h>
 
+#include <algorithm>
+
 #include "dfw_device.cuh"
 
 namespace dfw {
 namespace {
+
+// ------------------------------------------------------- clusters and launches
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The address of this CTA's shared word `a` in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t map_rank(uint32_t a, uint32_t rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ uint32_t ld_cluster(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ void st_cluster(uint32_t a, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+__device__ __forceinline__ void st_cluster_f32(uint32_t a, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
+}
+
+// A launch that may be a programmatic dependent of the one before (the kernel
+// then waits for that itself) or run in clusters.
+template <typename F, typename... A>
+dfw_status launch_with(F fn, uint64_t grid, unsigned block, uint32_t smem, bool dependent, unsigned cluster, cudaStream_t s,
+                       A... args) {
+    if (grid > 0x7FFFFFFFull) return DFW_EINVAL;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    cfg.attrs = attr;
+    cfg.numAttrs = 0;
+    if (dependent) {
+        attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (cluster > 1u) {
+        attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+        attr[cfg.numAttrs].val.clusterDim.x = cluster;
+        attr[cfg.numAttrs].val.clusterDim.y = 1;
+        attr[cfg.numAttrs++].val.clusterDim.z = 1;
+    }
+    return cudaLaunchKernelEx(&cfg, fn, args...) == cudaSuccess ? DFW_OK : DFW_ECUDA;
+}
+
+// ----------------------------------------------------------------- 4-bit tiles
 
 constexpr uint32_t Q4_ROWS = 16, Q4_COLS = 128, Q4_CODES = 1024;
 
@@ -161,6 +215,24 @@ __global__ void __launch_bounds__(256) q4_dequantise_tiles(const uint8_t *__rest
     }
 }
 
+// y = W x.  The products run on the matrix instruction m16n8k16: a tile's 16
+// rows are its rows, up to 8 vectors its columns (unused columns repeat the
+// last vector and are dropped), so 1 to 8 vectors cost the same and the codes
+// are expanded once for all.  A code's four bits ORed into the bf16 128 give
+// 128 + q exactly; subtracting 128 + z leaves q - z, exact, and a group's
+// products are summed by the instruction in fp32 before its scale multiplies
+// the sum (a bf16 weight s (q - z) would round).  Columns of a word are taken
+// in the order 0 4 1 5 2 6 3 7, in which the expansion yields them; the
+// vectors are laid out in shared memory to match.
+//
+// A warp walks tiles along the columns, four in flight in registers (one
+// 16-byte load per row half).  WK warps share a row tile's columns and add
+// their sums through shared memory in a fixed order, 16 / WK row tiles side
+// by side in a CTA; when the vectors are too long for one SM's shared memory
+// a cluster of 2 to 8 CTAs shares the columns the same way.
+constexpr uint32_t Q4_WARPS = 16, Q4_DEPTH = 4;
+constexpr uint32_t Q4_JOIN_BYTES = 32u * 1024u;  // a CTA's buffer for its cluster's sums
+
 struct Q4GemvParams {
     Q4Params q;
     const uint8_t *packed;
@@ -168,33 +240,271 @@ struct Q4GemvParams {
     void *y;
     uint64_t ldx, ldy;
     uint32_t m, y_fp32;
+    uint32_t wk;       // warps along the columns of a row tile
+    uint32_t split;    // CTAs along them (the cluster)
+    uint32_t tiles;    // column tiles per CTA
+    uint32_t pitch;    // bytes from one vector to the next in shared memory
+    uint32_t rounds;   // row tiles per group of wk warps
+    uint32_t batch;    // rounds between two joins of the cluster's sums
+    uint32_t xvec;     // the vectors can be read 16 bytes at a time
 };
 
-// y[m, n] = sum over groups of s (sum of (q - z) x), one thread per element.
-__global__ void __launch_bounds__(256) q4_gemv_plain(const Q4GemvParams a) {
-    const Q4Params &p = a.q;
-    for (uint64_t i = blockIdx.x * 256ull + threadIdx.x; i < (uint64_t)p.rows * a.m; i += gridDim.x * 256ull) {
-        const uint32_t n = (uint32_t)(i % p.rows), m = (uint32_t)(i / p.rows), r = n % Q4_ROWS;
-        const uint16_t *x = a.x + m * a.ldx;
-        float y = 0.f;
-        for (uint32_t ct = 0; ct < p.col_tiles; ++ct) {
-            const uint8_t *tile = a.packed + ((uint64_t)(n / Q4_ROWS) * p.col_tiles + ct) * p.tile_bytes;
-            const uint32_t span = Q4_COLS / p.gt;
-            for (uint32_t gi = 0; gi < p.gt && ct * Q4_COLS + gi * span < p.cols; ++gi) {
-                const float s = __uint_as_float((uint32_t)reinterpret_cast<const uint16_t *>(tile + Q4_CODES)[r * p.gt + gi] << 16);
-                const int z = p.zeros ? tile[Q4_CODES + 32u * p.gt + r * p.gt + gi] : 8;
-                float sum = 0.f;
-                for (uint32_t c = gi * span; c < (gi + 1u) * span; c += 8u) {
-                    const uint32_t word = *reinterpret_cast<const uint32_t *>(tile + q4_word_at(r, c));
-                    for (uint32_t j = 0; j < 8u; ++j)
-                        sum += (float)((int)((word >> (4u * j)) & 15u) - z) *
-                               __uint_as_float((uint32_t)x[ct * Q4_COLS + c + j] << 16);
-                }
-                y += s * sum;
+__device__ __forceinline__ uint4 ldg_stream(const void *p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Codes i and i + 4 of a word as two bf16, less `off` (128 + z in both).
+__device__ __forceinline__ uint32_t q4_pair(uint32_t word, int i, uint32_t off) {
+    const uint32_t v = ((word >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
+    uint32_t r;
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(off));
+    return r;
+}
+
+// A tile as one lane holds it: its words of both row halves, and the scales
+// and zero points of rows g and g + 8.
+template <int GT, bool Z>
+struct Q4Tile {
+    uint4 lo, hi;
+    uint32_t s[GT == 4 ? 4 : 2];  // GT = 4: two words per row, else one
+    uint32_t z[Z ? 2 : 1];
+    __device__ __forceinline__ void load(const uint8_t *tile, uint32_t lane) {
+        const uint32_t g = lane >> 2;
+        lo = ldg_stream(tile + 16u * lane);
+        hi = ldg_stream(tile + 512u + 16u * lane);
+        const uint8_t *sp = tile + Q4_CODES + 2u * GT * g, *zp = tile + Q4_CODES + 32u * GT + GT * g;
+        if constexpr (GT == 4) {
+            const uint2 a = __ldg(reinterpret_cast<const uint2 *>(sp)), b = __ldg(reinterpret_cast<const uint2 *>(sp + 64));
+            s[0] = a.x, s[1] = a.y, s[2] = b.x, s[3] = b.y;
+        } else if constexpr (GT == 2) {
+            s[0] = __ldg(reinterpret_cast<const uint32_t *>(sp));
+            s[1] = __ldg(reinterpret_cast<const uint32_t *>(sp + 32));
+        } else {
+            s[0] = __ldg(reinterpret_cast<const uint16_t *>(sp));
+            s[1] = __ldg(reinterpret_cast<const uint16_t *>(sp + 16));
+        }
+        if constexpr (Z) {
+            if constexpr (GT == 4) {
+                z[0] = __ldg(reinterpret_cast<const uint32_t *>(zp));
+                z[1] = __ldg(reinterpret_cast<const uint32_t *>(zp + 32));
+            } else if constexpr (GT == 2) {
+                z[0] = __ldg(reinterpret_cast<const uint16_t *>(zp));
+                z[1] = __ldg(reinterpret_cast<const uint16_t *>(zp + 16));
+            } else {
+                z[0] = __ldg(zp);
+                z[1] = __ldg(zp + 8);
             }
         }
-        if (a.y_fp32) static_cast<float *>(a.y)[m * a.ldy + n] = y;
-        else static_cast<__nv_bfloat16 *>(a.y)[m * a.ldy + n] = __float2bfloat16_rn(y);
+    }
+    __device__ __forceinline__ float scale(int half, int gi) const {
+        const uint32_t w = GT == 4 ? s[2 * half + (gi >> 1)] : s[half];
+        return __uint_as_float(gi & 1 ? w & 0xFFFF0000u : w << 16);
+    }
+    __device__ __forceinline__ uint32_t offset(int half, int gi) const {
+        if constexpr (!Z) return 0x43084308u;  // 136
+        else return 0x43004300u | ((z[half] >> (8 * gi)) & 0xFu) * 0x10001u;
+    }
+};
+
+// acc += the tile's products with NT x 8 vectors, whose words for its columns
+// start at shared address xs (+ 64 per word of codes, + nt_step per 8 vectors).
+template <int GT, bool Z, int NT>
+__device__ __forceinline__ void q4_tile_products(const Q4Tile<GT, Z> &b, uint32_t xs, uint32_t nt_step, float (&acc)[NT][4]) {
+    const uint32_t lo[4] = {b.lo.x, b.lo.y, b.lo.z, b.lo.w}, hi[4] = {b.hi.x, b.hi.y, b.hi.z, b.hi.w};
+#pragma unroll
+    for (int gi = 0; gi < GT; ++gi) {
+        float sum[NT][4] = {};
+        const uint32_t off0 = b.offset(0, gi), off1 = b.offset(1, gi);
+#pragma unroll
+        for (int w = gi * 4 / GT; w < (gi + 1) * 4 / GT; ++w) {
+            uint32_t l[4], h[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                l[i] = q4_pair(lo[w], i, off0);
+                h[i] = q4_pair(hi[w], i, off1);
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const uint4 x = lds128(xs + 64u * w + nt * nt_step);
+                mma_bf16(sum[nt], l[0], h[0], l[1], h[1], x.x, x.y);
+                mma_bf16(sum[nt], l[2], h[2], l[3], h[3], x.z, x.w);
+            }
+        }
+        const float s0 = b.scale(0, gi), s1 = b.scale(1, gi);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            acc[nt][0] = fmaf(s0, sum[nt][0], acc[nt][0]);
+            acc[nt][1] = fmaf(s0, sum[nt][1], acc[nt][1]);
+            acc[nt][2] = fmaf(s1, sum[nt][2], acc[nt][2]);
+            acc[nt][3] = fmaf(s1, sum[nt][3], acc[nt][3]);
+        }
+    }
+}
+
+__device__ __forceinline__ void q4_store(const Q4GemvParams &a, uint64_t row, uint32_t col, float v) {
+    if (row >= a.q.rows) return;
+    if (a.y_fp32) static_cast<float *>(a.y)[col * a.ldy + row] = v;
+    else static_cast<__nv_bfloat16 *>(a.y)[col * a.ldy + row] = __float2bfloat16_rn(v);
+}
+
+// Shared memory: the vectors | the warps' sums, two buffers | [clusters] the
+// sums of the cluster's CTAs.
+template <int GT, bool Z, int NT>
+__global__ void __launch_bounds__(32 * Q4_WARPS, 1) q4_gemv_tiles(const Q4GemvParams a) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    constexpr uint32_t OUT = 16u * 8u * NT;  // sums of a row tile
+    const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3u;
+    const uint32_t rank = blockIdx.x % a.split, group = warp / a.wk, k = warp % a.wk, groups = Q4_WARPS / a.wk;
+    const uint32_t ct0 = rank * a.tiles, cts = ct0 < a.q.col_tiles ? min(a.tiles, a.q.col_tiles - ct0) : 0u;
+    const uint32_t lo = k * cts / a.wk, hi = (k + 1u) * cts / a.wk;  // this warp's column tiles, from ct0
+    const uint64_t rt0 = (uint64_t)(blockIdx.x / a.split) * groups + group, stride = (uint64_t)(gridDim.x / a.split) * groups;
+    const uint32_t mine = rt0 < a.q.row_tiles ? (uint32_t)((a.q.row_tiles - 1u - rt0) / stride) + 1u : 0u;  // row tiles
+    float *part = reinterpret_cast<float *>(smem + a.m * a.pitch), *join = part + 2u * Q4_WARPS * OUT;
+    part += group * a.wk * OUT;
+
+    // the first tiles are on their way while the vectors are laid out
+    Q4Tile<GT, Z> buf[Q4_DEPTH];
+    const uint32_t per = hi - lo;
+    const uint64_t total = (uint64_t)mine * per;
+    const uint64_t row_step = stride * a.q.col_tiles * a.q.tile_bytes - (uint64_t)per * a.q.tile_bytes;
+    const uint8_t *next = a.packed + (rt0 * a.q.col_tiles + ct0 + lo) * a.q.tile_bytes;
+    uint32_t next_ct = 0;
+    uint64_t left = total;
+    auto fetch = [&](Q4Tile<GT, Z> &b) {
+        if (left == 0u) return;
+        b.load(next, lane);
+        --left;
+        next += a.q.tile_bytes;
+        if (++next_ct == per) {
+            next_ct = 0;
+            next += row_step;
+        }
+    };
+#pragma unroll
+    for (uint32_t u = 0; u < Q4_DEPTH; ++u) fetch(buf[u]);
+
+    // the vectors' columns [128 ct0, 128 (ct0 + cts)), zeros past the matrix
+    const uint32_t units = 16u * cts;
+    for (uint32_t i = threadIdx.x; i < units * a.m; i += 32u * Q4_WARPS) {
+        const uint32_t v = i / units, c = i % units, col = Q4_COLS * ct0 + 8u * c;
+        uint4 x = make_uint4(0u, 0u, 0u, 0u);
+        if (col < a.q.cols) {
+            const uint16_t *src = a.x + v * a.ldx + col;
+            if (a.xvec) {
+                x = __ldg(reinterpret_cast<const uint4 *>(src));
+            } else {
+                uint32_t e[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) e[j] = __ldg(src + j);
+                x = make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
+            }
+        }
+        *reinterpret_cast<uint4 *>(smem + v * a.pitch + 16u * c) =
+            make_uint4(__byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632), __byte_perm(x.y, x.w, 0x5410),
+                       __byte_perm(x.y, x.w, 0x7632));
+    }
+    if (a.split > 1u) cluster_sync();  // (and the other CTAs run: their shared memory can be written)
+    else __syncthreads();
+
+    const uint32_t x0 = smem_u32(smem) + min(g, a.m - 1u) * a.pitch + 16u * t;
+    const uint32_t nt_step = NT > 1 ? (min(g + 8u, a.m - 1u) - min(g, a.m - 1u)) * a.pitch : 0u;
+    float acc[NT][4] = {};
+    uint32_t round = 0;
+
+    // the end of a row tile: the group's sums, added in the warps' order
+    auto finish = [&]() {
+        float *p = part + (round & 1u) * Q4_WARPS * OUT + k * OUT;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {  // column-major: element (row, col) at 16 col + row
+            float *q = p + 128u * nt + 32u * t + g;
+            q[0] = acc[nt][0];
+            q[16] = acc[nt][1];
+            q[8] = acc[nt][2];
+            q[24] = acc[nt][3];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[nt][i] = 0.f;
+        }
+        if (a.wk == 1u) __syncwarp();
+        else asm volatile("bar.sync %0, %1;" ::"r"(1u + group), "r"(32u * a.wk) : "memory");  // at most 8 groups
+        const float *r = part + (round & 1u) * Q4_WARPS * OUT;
+        const uint64_t rt = rt0 + round * stride;
+        for (uint32_t o = 32u * k + lane; o < 16u * a.m; o += 32u * a.wk) {
+            float v = r[o];
+            for (uint32_t w = 1; w < a.wk; ++w) v += r[w * OUT + o];
+            if (a.split == 1u) {
+                q4_store(a, Q4_ROWS * rt + (o & 15u), o >> 4, v);
+            } else {  // to the CTA of the cluster that adds this round's
+                const uint32_t slot = (round % a.batch / a.split * groups + group) * a.split + rank;
+                st_cluster_f32(map_rank(smem_u32(join + slot * 16u * a.m + o), round % a.split), v);
+            }
+        }
+        ++round;
+    };
+    // every `batch` rounds the cluster's CTAs add each other's sums, in order
+    auto meet = [&](uint32_t from) {
+        cluster_sync();
+        for (uint32_t i = threadIdx.x; i < a.batch / a.split * groups * 16u * a.m; i += 32u * Q4_WARPS) {
+            const uint32_t o = i % (16u * a.m), gr = i / (16u * a.m) % groups, rd = i / (16u * a.m) / groups * a.split + rank;
+            const uint64_t rt = (uint64_t)(blockIdx.x / a.split) * groups + gr + (from + rd) * stride;
+            if (from + rd >= a.rounds || rt >= a.q.row_tiles) continue;
+            const float *r = join + (rd / a.split * groups + gr) * a.split * 16u * a.m + o;
+            float v = r[0];
+            for (uint32_t w = 1; w < a.split; ++w) v += r[w * 16u * a.m];
+            q4_store(a, Q4_ROWS * rt + (o & 15u), o >> 4, v);
+        }
+        cluster_sync();
+    };
+
+    if (a.split == 1u) {
+        uint32_t ct = lo;
+        for (uint64_t i = 0; i < total; i += Q4_DEPTH) {
+#pragma unroll
+            for (uint32_t u = 0; u < Q4_DEPTH; ++u) {
+                if (i + u >= total) break;
+                q4_tile_products<GT, Z, NT>(buf[u], x0 + 256u * ct, nt_step, acc);
+                fetch(buf[u]);
+                if (++ct == hi) {
+                    ct = lo;
+                    finish();
+                }
+            }
+        }
+        if (per == 0u)
+            while (round < mine) finish();
+        return;
+    }
+    // in a cluster every group takes part in every meeting
+    uint32_t ct = lo, met = 0;
+    uint64_t i = 0;
+    while (met < a.rounds) {
+        const uint32_t until = min(met + a.batch, mine);
+        while (round < until) {
+            if (per == 0u) {
+                finish();
+                continue;
+            }
+#pragma unroll
+            for (uint32_t u = 0; u < Q4_DEPTH; ++u) {
+                if ((uint32_t)(i % Q4_DEPTH) != u || round >= until) continue;
+                q4_tile_products<GT, Z, NT>(buf[u], x0 + 256u * ct, nt_step, acc);
+                fetch(buf[u]);
+                ++i;
+                if (++ct == hi) {
+                    ct = lo;
+                    finish();
+                }
+            }
+        }
+        meet(met);
+        met += a.batch;
     }
 }
 
@@ -275,10 +585,96 @@ dfw_status launch_q4_dequantise(const uint8_t *d_packed, const dfw_q4_info *info
     return cudaGetLastError() == cudaSuccess ? DFW_OK : DFW_ECUDA;
 }
 
+namespace {
+
+// How a product is cut: wk and split by the time they give, counted in tiles
+// a warp walks (a row tile's sums cost about half a tile more).  The matrices
+// of one step are too small to be cut blindly: 4096 rows are 256 row tiles,
+// 1.7 per SM, and two of them in turn on some SMs would take as long as two on
+// all.
+void q4_cut(Q4GemvParams &a, uint32_t split, uint32_t ctas) {
+    a.split = split;
+    a.tiles = (a.q.col_tiles + split - 1u) / split;
+    uint64_t best = ~0ull;
+    for (uint32_t wk = 1; wk <= Q4_WARPS; wk *= 2u) {
+        const uint64_t at_once = (uint64_t)(ctas / split) * (Q4_WARPS / wk), rounds = (a.q.row_tiles + at_once - 1u) / at_once;
+        const uint64_t cost = rounds * (2u * ((a.tiles + wk - 1u) / wk) + 1u);
+        if (cost < best) {
+            best = cost;
+            a.wk = wk;
+            a.rounds = (uint32_t)rounds;
+        }
+    }
+}
+
+typedef void (*q4_fn)(const Q4GemvParams);
+template <int GT, bool Z>
+q4_fn q4_variant(uint32_t m) {
+    return m > 8u ? q4_gemv_tiles<GT, Z, 2> : q4_gemv_tiles<GT, Z, 1>;
+}
+q4_fn q4_variant(const Q4Params &q, uint32_t m) {
+    switch (q.gt) {
+        case 1: return q.zeros ? q4_variant<1, true>(m) : q4_variant<1, false>(m);
+        case 2: return q.zeros ? q4_variant<2, true>(m) : q4_variant<2, false>(m);
+        default: return q.zeros ? q4_variant<4, true>(m) : q4_variant<4, false>(m);
+    }
+}
+
+constexpr uint32_t SMEM_MOST = 227u * 1024u;
+
+dfw_status launch_q4_pass(Q4GemvParams a, int dev, int sms, cudaStream_t s) {
+    const q4_fn fn = q4_variant(a.q, a.m);
+    const uint32_t sums = 2u * Q4_WARPS * 128u * (a.m > 8u ? 2u : 1u) * 4u;
+    // as few CTAs to a row tile as their shared memory allows
+    uint32_t split = 1, x_bytes = 0;
+    for (;; split *= 2u) {
+        const uint32_t tiles = (a.q.col_tiles + split - 1u) / split;
+        a.pitch = tiles * 2u * Q4_COLS + 64u;  // neighbouring vectors 16 banks apart
+        x_bytes = a.m * a.pitch;
+        if (x_bytes + sums + (split > 1u ? Q4_JOIN_BYTES : 0u) <= SMEM_MOST) break;
+        if (split == 8u) return DFW_EINVAL;  // (not reached: the caller bounds m by cols)
+    }
+    const uint32_t smem = x_bytes + sums + (split > 1u ? Q4_JOIN_BYTES : 0u);
+    static bool opted[16][12];
+    const uint32_t vi = (a.q.gt == 1u ? 0u : a.q.gt == 2u ? 1u : 2u) * 4u + a.q.zeros * 2u + (a.m > 8u ? 1u : 0u);
+    if (!opted[dev][vi]) {
+        if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MOST) != cudaSuccess) return DFW_ECUDA;
+        opted[dev][vi] = true;
+    }
+    uint32_t ctas = (uint32_t)sms;
+    if (split > 1u) {  // clusters that find room at once: not every SM can be in one
+        static int room[16][9];
+        if (!room[dev][split]) {
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(split);
+            cfg.blockDim = dim3(32u * Q4_WARPS);
+            cfg.dynamicSmemBytes = SMEM_MOST;
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = split;
+            attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            int n = 0;
+            if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess || n < 1) return DFW_ECUDA;
+            room[dev][split] = n;
+        }
+        ctas = (uint32_t)room[dev][split] * split;
+    }
+    q4_cut(a, split, ctas);
+    const uint32_t groups = Q4_WARPS / a.wk;
+    const uint64_t clusters = std::min<uint64_t>(ctas / split, (a.q.row_tiles + groups - 1u) / groups);
+    a.batch = split;
+    while (a.batch < a.rounds && (a.batch / split + 1u) * groups * split * 16u * a.m * 4u <= Q4_JOIN_BYTES) a.batch += split;
+    return launch_with(fn, clusters * split, 32u * Q4_WARPS, smem, false, split, s, a);
+}
+
+}  // namespace
+
 dfw_status launch_q4_gemv(const uint8_t *d_packed, const dfw_q4_info *info, uint32_t m, const uint16_t *d_x,
                           uint64_t ldx, void *d_y, int y_fp32, uint64_t ldy, cudaStream_t s) {
     Q4GemvParams a;
-    int sms = 0;
+    int sms = 0, dev = 0;
     dfw_status st = q4_checked(info, d_packed, a.q);
     if (st != DFW_OK) return st;
     if (m > DFW_Q4_MAX_VECTORS || (m && (!d_x || !d_y)) || (m > 1u && (ldx < a.q.cols || ldy < a.q.rows)) ||
@@ -287,16 +683,21 @@ dfw_status launch_q4_gemv(const uint8_t *d_packed, const dfw_q4_info *info, uint
     if ((reinterpret_cast<uintptr_t>(d_x) & 1u) || (reinterpret_cast<uintptr_t>(d_y) & (y_fp32 ? 3u : 1u))) return DFW_EALIGN;
     if (m == 0u) return DFW_OK;
     if ((st = device_sms(sms)) != DFW_OK) return st;
+    if (cudaGetDevice(&dev) != cudaSuccess) return DFW_ECUDA;
     a.packed = d_packed;
-    a.x = d_x;
-    a.y = d_y;
     a.ldx = ldx;
     a.ldy = ldy;
-    a.m = m;
     a.y_fp32 = (uint32_t)y_fp32;
-    const uint64_t want = ((uint64_t)a.q.rows * m + 255u) / 256u, cap = (uint64_t)sms * 16u;
-    q4_gemv_plain<<<(unsigned)(want < cap ? want : cap), 256, 0, s>>>(a);
-    return cudaGetLastError() == cudaSuccess ? DFW_OK : DFW_ECUDA;
+    a.xvec = (reinterpret_cast<uintptr_t>(d_x) & 15u) == 0u && (m == 1u || ldx % 8u == 0u);
+    // 16 vectors a pass, or 8 where 16 would not fit the eight CTAs of the largest cluster
+    const uint32_t most = a.q.col_tiles <= 272u ? 16u : 8u;
+    for (uint32_t j = 0; j < m; j += most) {
+        a.m = std::min(most, m - j);
+        a.x = d_x + j * ldx;
+        a.y = static_cast<uint8_t *>(d_y) + j * ldy * (y_fp32 ? 4u : 2u);
+        if ((st = launch_q4_pass(a, dev, sms, s)) != DFW_OK) return st;
+    }
+    return DFW_OK;
 }
 
 }  // namespace dfw
