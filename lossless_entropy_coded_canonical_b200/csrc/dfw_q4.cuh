@@ -10,10 +10,12 @@
 // Layout.  A tile is 16 rows x 128 columns, stored as one contiguous piece:
 //   1024 bytes of codes: row half h (rows 8 h + g), lane l = 4 g + t, word w
 //        (0..3) at 512 h + 16 l + 4 w holds row 8 h + g, columns 32 w + 8 t +
-//        i in bits 4 i .. 4 i + 3.  A lane of the multiplying warp thus gets
-//        one 16-byte load per row half, a warp's load is 512 contiguous
-//        bytes, and word w of every lane lies in columns 32 w .. 32 w + 31, so
-//        each matrix instruction stays inside one group even at G = 32;
+//        0..7: the even ones in its low half, the odd ones in its high half,
+//        so that one mask takes two neighbours into a register's two halves.
+//        A lane of the multiplying warp thus gets one 16-byte load per row
+//        half, a warp's load is 512 contiguous bytes, and word w of every lane
+//        lies in columns 32 w .. 32 w + 31, so each matrix instruction stays
+//        inside one group even at G = 32;
 //   32 GT bytes of scales (GT = 128 / G groups): row r's GT bf16 at 2 GT r;
 //   16 GT bytes of zero points, if any: row r's GT bytes at GT r.
 // Tiles follow each other along the columns, then down the rows.  Rows and
@@ -98,6 +100,15 @@ __device__ __forceinline__ uint32_t q4_word_at(uint32_t r, uint32_t c) {
     return 512u * (r >> 3) + 16u * (4u * (r & 7u) + ((c >> 3) & 3u)) + 4u * (c >> 5);
 }
 
+// Eight codes in column order (column i in bits 4 i .. 4 i + 3) -> even ones
+// in the low half, odd ones in the high half.
+__device__ __forceinline__ uint32_t q4_split(uint32_t w) {
+    uint32_t e = w & 0x0F0F0F0Fu, o = (w >> 4) & 0x0F0F0F0Fu;
+    e = (e | e >> 4) & 0x00FF00FFu;
+    o = (o | o >> 4) & 0x00FF00FFu;
+    return ((e | e >> 8) & 0xFFFFu) | (o | o >> 8) << 16;
+}
+
 // Row-major codes (two to a byte, even column in the low half), scales and
 // zero points -> tiles.  One thread per word of codes; the first threads of a
 // tile also place its scales and zero points.
@@ -113,7 +124,7 @@ __global__ void __launch_bounds__(256) q4_pack_tiles(const uint8_t *__restrict__
         const uint32_t r = threadIdx.x >> 4, c = 8u * (threadIdx.x & 15u);
         uint32_t word = p.zeros ? 0u : 0x88888888u;
         if (r0 + r < p.rows && c0 + c < p.cols)
-            word = __ldg(reinterpret_cast<const uint32_t *>(codes + ((r0 + r) * p.cols + c0 + c) / 2u));
+            word = q4_split(__ldg(reinterpret_cast<const uint32_t *>(codes + ((r0 + r) * p.cols + c0 + c) / 2u)));
         *reinterpret_cast<uint32_t *>(dst + q4_word_at(r, c)) = word;
         if (threadIdx.x < Q4_ROWS * p.gt) {
             const uint32_t rr = threadIdx.x / p.gt, gi = threadIdx.x % p.gt;
@@ -176,12 +187,12 @@ __global__ void __launch_bounds__(512) q4_quantise_tiles(const uint16_t *__restr
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float q = live ? rintf(v[i] / s) + zp : zp;
-            half |= (uint32_t)fminf(fmaxf(q, 0.f), 15.f) << (4 * i);
+            half |= (uint32_t)fminf(fmaxf(q, 0.f), 15.f) << (16 * (i & 1) + 4 * (i >> 1));
         }
-        if (!in) half = p.zeros ? 0u : 0x8888u;
+        if (!in) half = p.zeros ? 0u : 0x00880088u;
         const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, half, 1);
         uint8_t *dst = out + tile * p.tile_bytes;
-        if (!(lane & 1u)) *reinterpret_cast<uint32_t *>(dst + q4_word_at(r, 4u * lane)) = half | (other << 16);
+        if (!(lane & 1u)) *reinterpret_cast<uint32_t *>(dst + q4_word_at(r, 4u * lane)) = half | (other << 8);
         if (lane % span == 0u) {
             const uint32_t gi = lane / span;
             reinterpret_cast<uint16_t *>(dst + Q4_CODES)[r * p.gt + gi] = in ? __bfloat16_as_ushort(sb) : (uint16_t)0;
@@ -206,8 +217,8 @@ __global__ void __launch_bounds__(256) q4_dequantise_tiles(const uint8_t *__rest
         uint32_t v[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float a = s * (float)((int)((word >> (8 * i)) & 15u) - z);
-            const float b = s * (float)((int)((word >> (8 * i + 4)) & 15u) - z);
+            const float a = s * (float)((int)((word >> (4 * i)) & 15u) - z);
+            const float b = s * (float)((int)((word >> (4 * i + 16)) & 15u) - z);
             v[i] = (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(a)) |
                    ((uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(b)) << 16);
         }
@@ -218,12 +229,14 @@ __global__ void __launch_bounds__(256) q4_dequantise_tiles(const uint8_t *__rest
 // y = W x.  The products run on the matrix instruction m16n8k16: a tile's 16
 // rows are its rows, up to 8 vectors its columns (unused columns repeat the
 // last vector and are dropped), so 1 to 8 vectors cost the same and the codes
-// are expanded once for all.  A code's four bits ORed into the bf16 128 give
-// 128 + q exactly; subtracting 128 + z leaves q - z, exact, and a group's
-// products are summed by the instruction in fp32 before its scale multiplies
-// the sum (a bf16 weight s (q - z) would round).  Columns of a word are taken
-// in the order 0 4 1 5 2 6 3 7, in which the expansion yields them; the
-// vectors are laid out in shared memory to match.
+// are expanded once for all.  Expanding is what the kernel is short of
+// instructions for, so it takes two per pair of codes and half a shift: a
+// masked code in bits 0..3 or 4..7 of a bf16 is the number q 2^-133 or
+// 16 q 2^-133 (below 2^-125 a bf16's bits are a plain integer), so one
+// multiply-add with 2^127 or 2^123 and -z / 64 gives (q - z) / 64, exact.  A
+// group's products are summed by the instruction in fp32 before its scale
+// multiplies the sum (a bf16 weight s (q - z) would round); the 64 multiplies
+// the finished sum.
 //
 // A warp walks tiles along the columns, four in flight in registers (one
 // 16-byte load per row half).  WK warps share a row tile's columns and add
@@ -255,18 +268,31 @@ __device__ __forceinline__ uint4 ldg_stream(const void *p) {
     return v;
 }
 
-__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+// d = c + the products of a 16 x 16 and a 16 x 8 tile of bf16; `first`: c is 0.
+__device__ __forceinline__ void mma_bf16(float (&d)[4], bool first, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+    const float z = 0.f;
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(first ? z : d[0]), "f"(first ? z : d[1]),
+          "f"(first ? z : d[2]), "f"(first ? z : d[3]));
 }
 
-// Codes i and i + 4 of a word as two bf16, less `off` (128 + z in both).
-__device__ __forceinline__ uint32_t q4_pair(uint32_t word, int i, uint32_t off) {
-    const uint32_t v = ((word >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
     uint32_t r;
-    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(off));
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
     return r;
+}
+
+// A word's eight codes, less the zero point, over 64: columns 2 i and 2 i + 1
+// in the halves of e[i].  off: -z / 64 in both halves.
+__device__ __forceinline__ void q4_expand(uint32_t word, uint32_t off, uint32_t (&e)[4]) {
+    constexpr uint32_t LOW = 0x7F007F00u, HIGH = 0x7D007D00u;  // 2^127, 2^123
+    const uint32_t up = __umulhi(word, 1u << 24);              // word >> 8, on the multiply-add pipe
+    e[0] = fma_bf16x2(word & 0x000F000Fu, LOW, off);
+    e[1] = fma_bf16x2(word & 0x00F000F0u, HIGH, off);
+    e[2] = fma_bf16x2(up & 0x000F000Fu, LOW, off);
+    e[3] = fma_bf16x2(up & 0x00F000F0u, HIGH, off);
 }
 
 // A tile as one lane holds it: its words of both row halves, and the scales
@@ -276,11 +302,11 @@ struct Q4Tile {
     uint4 lo, hi;
     uint32_t s[GT == 4 ? 4 : 2];  // GT = 4: two words per row, else one
     uint32_t z[Z ? 2 : 1];
-    __device__ __forceinline__ void load(const uint8_t *tile, uint32_t lane) {
-        const uint32_t g = lane >> 2;
-        lo = ldg_stream(tile + 16u * lane);
-        hi = ldg_stream(tile + 512u + 16u * lane);
-        const uint8_t *sp = tile + Q4_CODES + 2u * GT * g, *zp = tile + Q4_CODES + 32u * GT + GT * g;
+    // cp: the lane's codes, tile + 16 lane; sp: row g's scales, tile + 1024 + 2 GT g
+    __device__ __forceinline__ void load(const uint8_t *cp, const uint8_t *sp, uint32_t g) {
+        lo = ldg_stream(cp);
+        hi = ldg_stream(cp + 512);
+        const uint8_t *zp = sp + 32u * GT - GT * g;
         if constexpr (GT == 4) {
             const uint2 a = __ldg(reinterpret_cast<const uint2 *>(sp)), b = __ldg(reinterpret_cast<const uint2 *>(sp + 64));
             s[0] = a.x, s[1] = a.y, s[2] = b.x, s[3] = b.y;
@@ -308,9 +334,9 @@ struct Q4Tile {
         const uint32_t w = GT == 4 ? s[2 * half + (gi >> 1)] : s[half];
         return __uint_as_float(gi & 1 ? w & 0xFFFF0000u : w << 16);
     }
-    __device__ __forceinline__ uint32_t offset(int half, int gi) const {
-        if constexpr (!Z) return 0x43084308u;  // 136
-        else return 0x43004300u | ((z[half] >> (8 * gi)) & 0xFu) * 0x10001u;
+    __device__ __forceinline__ uint32_t offset(int half, int gi) const {  // -z / 64
+        if constexpr (!Z) return 0xBE00BE00u;  // -8 / 64
+        else return fma_bf16x2(((z[half] >> (8 * gi)) & 0xFu) * 0x10001u, 0xFF00FF00u, 0x80008000u);  // z 2^-133 x -2^127
     }
 };
 
@@ -321,21 +347,19 @@ __device__ __forceinline__ void q4_tile_products(const Q4Tile<GT, Z> &b, uint32_
     const uint32_t lo[4] = {b.lo.x, b.lo.y, b.lo.z, b.lo.w}, hi[4] = {b.hi.x, b.hi.y, b.hi.z, b.hi.w};
 #pragma unroll
     for (int gi = 0; gi < GT; ++gi) {
-        float sum[NT][4] = {};
+        float sum[NT][4];
         const uint32_t off0 = b.offset(0, gi), off1 = b.offset(1, gi);
 #pragma unroll
         for (int w = gi * 4 / GT; w < (gi + 1) * 4 / GT; ++w) {
             uint32_t l[4], h[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                l[i] = q4_pair(lo[w], i, off0);
-                h[i] = q4_pair(hi[w], i, off1);
-            }
+            q4_expand(lo[w], off0, l);
+            q4_expand(hi[w], off1, h);
+            const bool first = w == gi * 4 / GT;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 const uint4 x = lds128(xs + 64u * w + nt * nt_step);
-                mma_bf16(sum[nt], l[0], h[0], l[1], h[1], x.x, x.y);
-                mma_bf16(sum[nt], l[2], h[2], l[3], h[3], x.z, x.w);
+                mma_bf16(sum[nt], first, l[0], h[0], l[1], h[1], x.x, x.y);
+                mma_bf16(sum[nt], false, l[2], h[2], l[3], h[3], x.z, x.w);
             }
         }
         const float s0 = b.scale(0, gi), s1 = b.scale(1, gi);
@@ -351,6 +375,7 @@ __device__ __forceinline__ void q4_tile_products(const Q4Tile<GT, Z> &b, uint32_
 
 __device__ __forceinline__ void q4_store(const Q4GemvParams &a, uint64_t row, uint32_t col, float v) {
     if (row >= a.q.rows) return;
+    v *= 64.f;
     if (a.y_fp32) static_cast<float *>(a.y)[col * a.ldy + row] = v;
     else static_cast<__nv_bfloat16 *>(a.y)[col * a.ldy + row] = __float2bfloat16_rn(v);
 }
@@ -373,19 +398,21 @@ __global__ void __launch_bounds__(32 * Q4_WARPS, 1) q4_gemv_tiles(const Q4GemvPa
     // the first tiles are on their way while the vectors are laid out
     Q4Tile<GT, Z> buf[Q4_DEPTH];
     const uint32_t per = hi - lo;
-    const uint64_t total = (uint64_t)mine * per;
+    const uint32_t total = mine * per;
     const uint64_t row_step = stride * a.q.col_tiles * a.q.tile_bytes - (uint64_t)per * a.q.tile_bytes;
-    const uint8_t *next = a.packed + (rt0 * a.q.col_tiles + ct0 + lo) * a.q.tile_bytes;
-    uint32_t next_ct = 0;
-    uint64_t left = total;
+    const uint8_t *first = a.packed + (rt0 * a.q.col_tiles + ct0 + lo) * a.q.tile_bytes;
+    const uint8_t *next_codes = first + 16u * lane, *next_scales = first + Q4_CODES + 2u * GT * g;
+    uint32_t row_left = per, left = total;
     auto fetch = [&](Q4Tile<GT, Z> &b) {
         if (left == 0u) return;
-        b.load(next, lane);
+        b.load(next_codes, next_scales, g);
         --left;
-        next += a.q.tile_bytes;
-        if (++next_ct == per) {
-            next_ct = 0;
-            next += row_step;
+        next_codes += a.q.tile_bytes;
+        next_scales += a.q.tile_bytes;
+        if (--row_left == 0u) {
+            row_left = per;
+            next_codes += row_step;
+            next_scales += row_step;
         }
     };
 #pragma unroll
@@ -395,22 +422,18 @@ __global__ void __launch_bounds__(32 * Q4_WARPS, 1) q4_gemv_tiles(const Q4GemvPa
     const uint32_t units = 16u * cts;
     for (uint32_t i = threadIdx.x; i < units * a.m; i += 32u * Q4_WARPS) {
         const uint32_t v = i / units, c = i % units, col = Q4_COLS * ct0 + 8u * c;
-        uint4 x = make_uint4(0u, 0u, 0u, 0u);
-        if (col < a.q.cols) {
-            const uint16_t *src = a.x + v * a.ldx + col;
-            if (a.xvec) {
-                x = __ldg(reinterpret_cast<const uint4 *>(src));
-            } else {
-                uint32_t e[8];
+        const uint16_t *src = a.x + v * a.ldx + col;
+        uint8_t *dst = smem + v * a.pitch + 16u * c;
+        if (col >= a.q.cols) {
+            *reinterpret_cast<uint4 *>(dst) = make_uint4(0u, 0u, 0u, 0u);
+        } else if (a.xvec) {
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+        } else {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) e[j] = __ldg(src + j);
-                x = make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
-            }
+            for (int j = 0; j < 8; ++j) reinterpret_cast<uint16_t *>(dst)[j] = __ldg(src + j);
         }
-        *reinterpret_cast<uint4 *>(smem + v * a.pitch + 16u * c) =
-            make_uint4(__byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632), __byte_perm(x.y, x.w, 0x5410),
-                       __byte_perm(x.y, x.w, 0x7632));
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
     if (a.split > 1u) cluster_sync();  // (and the other CTAs run: their shared memory can be written)
     else __syncthreads();
 
@@ -465,7 +488,7 @@ __global__ void __launch_bounds__(32 * Q4_WARPS, 1) q4_gemv_tiles(const Q4GemvPa
 
     if (a.split == 1u) {
         uint32_t ct = lo;
-        for (uint64_t i = 0; i < total; i += Q4_DEPTH) {
+        for (uint32_t i = 0; i < total; i += Q4_DEPTH) {
 #pragma unroll
             for (uint32_t u = 0; u < Q4_DEPTH; ++u) {
                 if (i + u >= total) break;
@@ -482,8 +505,7 @@ __global__ void __launch_bounds__(32 * Q4_WARPS, 1) q4_gemv_tiles(const Q4GemvPa
         return;
     }
     // in a cluster every group takes part in every meeting
-    uint32_t ct = lo, met = 0;
-    uint64_t i = 0;
+    uint32_t ct = lo, met = 0, i = 0;
     while (met < a.rounds) {
         const uint32_t until = min(met + a.batch, mine);
         while (round < until) {
@@ -493,7 +515,7 @@ __global__ void __launch_bounds__(32 * Q4_WARPS, 1) q4_gemv_tiles(const Q4GemvPa
             }
 #pragma unroll
             for (uint32_t u = 0; u < Q4_DEPTH; ++u) {
-                if ((uint32_t)(i % Q4_DEPTH) != u || round >= until) continue;
+                if (i % Q4_DEPTH != u || round >= until) continue;
                 q4_tile_products<GT, Z, NT>(buf[u], x0 + 256u * ct, nt_step, acc);
                 fetch(buf[u]);
                 ++i;
