@@ -238,13 +238,17 @@ __global__ void __launch_bounds__(256) q4_dequantise_tiles(const uint8_t *__rest
 // multiplies the sum (a bf16 weight s (q - z) would round); the 64 multiplies
 // the finished sum.
 //
-// A warp walks tiles along the columns, four in flight in registers (one
-// 16-byte load per row half).  WK warps share a row tile's columns and add
-// their sums through shared memory in a fixed order, 16 / WK row tiles side
-// by side in a CTA; when the vectors are too long for one SM's shared memory
-// a cluster of 2 to 8 CTAs shares the columns the same way.
-constexpr uint32_t Q4_WARPS = 16, Q4_DEPTH = 4;
-constexpr uint32_t Q4_JOIN_BYTES = 32u * 1024u;  // a CTA's buffer for its cluster's sums
+// A warp walks tiles along the columns, the next ones on their way into its
+// ring of tiles in shared memory (asynchronous copies: tiles in flight in
+// registers left room for half the warps).  WK warps share a row tile's columns
+// and add their sums through shared memory in a fixed order, W / WK row tiles
+// side by side in a CTA of W warps; when the vectors are too long for one SM's
+// shared memory a cluster of 2 to 8 CTAs shares the columns the same way.
+// Up to 8 vectors take 32 warps of 64 registers, or 16 where their shared
+// memory does not allow 32; 9 to 16 have twice the sums and take 16.
+constexpr uint32_t Q4_STEP = 2;                          // tiles a warp takes at a time
+constexpr uint32_t Q4_JOIN_BYTES = 16u * 1024u;          // a CTA's buffer for its cluster's sums
+__host__ __device__ constexpr uint32_t q4_ring(int nt, uint32_t warps) { return nt == 1 && warps == 16u ? 3u : 2u; }  // steps in a warp's ring
 
 struct Q4GemvParams {
     Q4Params q;
@@ -258,15 +262,28 @@ struct Q4GemvParams {
     uint32_t tiles;    // column tiles per CTA
     uint32_t pitch;    // bytes from one vector to the next in shared memory
     uint32_t rounds;   // row tiles per group of wk warps
-    uint32_t batch;    // rounds between two joins of the cluster's sums
+    uint32_t hold;     // row tiles a warp keeps its sums of before the group adds them up
+    uint32_t batch;    // rounds between two joins of the cluster's sums (a multiple of hold)
     uint32_t xvec;     // the vectors can be read 16 bytes at a time
 };
 
-__device__ __forceinline__ uint4 ldg_stream(const void *p) {
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
     return v;
 }
+__device__ __forceinline__ uint32_t lds8(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Waits until all but this thread's N newest groups of copies have landed.
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 // d = c + the products of a 16 x 16 and a 16 x 8 tile of bf16; `first`: c is 0.
 __device__ __forceinline__ void mma_bf16(float (&d)[4], bool first, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -295,40 +312,27 @@ __device__ __forceinline__ void q4_expand(uint32_t word, uint32_t off, uint32_t 
     e[3] = fma_bf16x2(up & 0x00F000F0u, HIGH, off);
 }
 
-// A tile as one lane holds it: its words of both row halves, and the scales
-// and zero points of rows g and g + 8.
+// A tile as one lane takes it from the ring (shared address `tile`): its words
+// of both row halves, and the scales and zero points of rows g and g + 8.
 template <int GT, bool Z>
 struct Q4Tile {
     uint4 lo, hi;
     uint32_t s[GT == 4 ? 4 : 2];  // GT = 4: two words per row, else one
     uint32_t z[Z ? 2 : 1];
-    // cp: the lane's codes, tile + 16 lane; sp: row g's scales, tile + 1024 + 2 GT g
-    __device__ __forceinline__ void load(const uint8_t *cp, const uint8_t *sp, uint32_t g) {
-        lo = ldg_stream(cp);
-        hi = ldg_stream(cp + 512);
-        const uint8_t *zp = sp + 32u * GT - GT * g;
+    __device__ __forceinline__ Q4Tile(uint32_t tile, uint32_t lane) {
+        const uint32_t g = lane >> 2, sp = tile + Q4_CODES + 2u * GT * g, zp = tile + Q4_CODES + 32u * GT + GT * g;
+        lo = lds128(tile + 16u * lane);
+        hi = lds128(tile + 512u + 16u * lane);
         if constexpr (GT == 4) {
-            const uint2 a = __ldg(reinterpret_cast<const uint2 *>(sp)), b = __ldg(reinterpret_cast<const uint2 *>(sp + 64));
-            s[0] = a.x, s[1] = a.y, s[2] = b.x, s[3] = b.y;
+            s[0] = lds32(sp), s[1] = lds32(sp + 4u), s[2] = lds32(sp + 64u), s[3] = lds32(sp + 68u);
         } else if constexpr (GT == 2) {
-            s[0] = __ldg(reinterpret_cast<const uint32_t *>(sp));
-            s[1] = __ldg(reinterpret_cast<const uint32_t *>(sp + 32));
+            s[0] = lds32(sp), s[1] = lds32(sp + 32u);
         } else {
-            s[0] = __ldg(reinterpret_cast<const uint16_t *>(sp));
-            s[1] = __ldg(reinterpret_cast<const uint16_t *>(sp + 16));
+            s[0] = lds16(sp), s[1] = lds16(sp + 16u);
         }
-        if constexpr (Z) {
-            if constexpr (GT == 4) {
-                z[0] = __ldg(reinterpret_cast<const uint32_t *>(zp));
-                z[1] = __ldg(reinterpret_cast<const uint32_t *>(zp + 32));
-            } else if constexpr (GT == 2) {
-                z[0] = __ldg(reinterpret_cast<const uint16_t *>(zp));
-                z[1] = __ldg(reinterpret_cast<const uint16_t *>(zp + 16));
-            } else {
-                z[0] = __ldg(zp);
-                z[1] = __ldg(zp + 8);
-            }
-        }
+        if constexpr (Z && GT == 4) z[0] = lds32(zp), z[1] = lds32(zp + 32u);
+        if constexpr (Z && GT == 2) z[0] = lds16(zp), z[1] = lds16(zp + 16u);
+        if constexpr (Z && GT == 1) z[0] = lds8(zp), z[1] = lds8(zp + 8u);
     }
     __device__ __forceinline__ float scale(int half, int gi) const {
         const uint32_t w = GT == 4 ? s[2 * half + (gi >> 1)] : s[half];
@@ -380,153 +384,156 @@ __device__ __forceinline__ void q4_store(const Q4GemvParams &a, uint64_t row, ui
     else static_cast<__nv_bfloat16 *>(a.y)[col * a.ldy + row] = __float2bfloat16_rn(v);
 }
 
-// Shared memory: the vectors | the warps' sums, two buffers | [clusters] the
-// sums of the cluster's CTAs.
-template <int GT, bool Z, int NT>
-__global__ void __launch_bounds__(32 * Q4_WARPS, 1) q4_gemv_tiles(const Q4GemvParams a) {
+// Shared memory: the warps' rings | the warps' sums | the vectors | [clusters]
+// the sums of the cluster's CTAs.
+template <int GT, bool Z, int NT, uint32_t W, bool SPLIT>
+__global__ void __launch_bounds__(32 * W, 1) q4_gemv_tiles(const Q4GemvParams a) {
     extern __shared__ __align__(16) uint8_t smem[];
-    constexpr uint32_t OUT = 16u * 8u * NT;  // sums of a row tile
+    constexpr uint32_t TILE = Q4_CODES + 32u * GT + (Z ? 16u * GT : 0u), SLOT = Q4_STEP * TILE, RING = q4_ring(NT, W);
+    const uint32_t outs = 16u * a.m;  // sums of a row tile, column by column
     const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3u;
-    const uint32_t rank = blockIdx.x % a.split, group = warp / a.wk, k = warp % a.wk, groups = Q4_WARPS / a.wk;
+    const uint32_t split = SPLIT ? a.split : 1u, rank = blockIdx.x % split;
+    const uint32_t group = warp / a.wk, k = warp % a.wk, groups = W / a.wk;
     const uint32_t ct0 = rank * a.tiles, cts = ct0 < a.q.col_tiles ? min(a.tiles, a.q.col_tiles - ct0) : 0u;
-    const uint32_t lo = k * cts / a.wk, hi = (k + 1u) * cts / a.wk;  // this warp's column tiles, from ct0
-    const uint64_t rt0 = (uint64_t)(blockIdx.x / a.split) * groups + group, stride = (uint64_t)(gridDim.x / a.split) * groups;
+    const uint32_t lo = k * cts / a.wk, hi = (k + 1u) * cts / a.wk, per = hi - lo;  // this warp's column tiles, from ct0
+    const uint64_t rt0 = (uint64_t)(blockIdx.x / split) * groups + group, stride = (uint64_t)(gridDim.x / split) * groups;
     const uint32_t mine = rt0 < a.q.row_tiles ? (uint32_t)((a.q.row_tiles - 1u - rt0) / stride) + 1u : 0u;  // row tiles
-    float *part = reinterpret_cast<float *>(smem + a.m * a.pitch), *join = part + 2u * Q4_WARPS * OUT;
-    part += group * a.wk * OUT;
+    const uint32_t ring = smem_u32(smem) + warp * RING * SLOT;
+    float *sums = reinterpret_cast<float *>(smem + W * RING * SLOT);
+    uint8_t *vecs = reinterpret_cast<uint8_t *>(sums + W * a.hold * outs);
+    float *join = reinterpret_cast<float *>(vecs + a.m * a.pitch);
 
-    // the first tiles are on their way while the vectors are laid out
-    Q4Tile<GT, Z> buf[Q4_DEPTH];
-    const uint32_t per = hi - lo;
-    const uint32_t total = mine * per;
-    const uint64_t row_step = stride * a.q.col_tiles * a.q.tile_bytes - (uint64_t)per * a.q.tile_bytes;
-    const uint8_t *first = a.packed + (rt0 * a.q.col_tiles + ct0 + lo) * a.q.tile_bytes;
-    const uint8_t *next_codes = first + 16u * lane, *next_scales = first + Q4_CODES + 2u * GT * g;
-    uint32_t row_left = per, left = total;
-    auto fetch = [&](Q4Tile<GT, Z> &b) {
-        if (left == 0u) return;
-        b.load(next_codes, next_scales, g);
-        --left;
-        next_codes += a.q.tile_bytes;
-        next_scales += a.q.tile_bytes;
-        if (--row_left == 0u) {
-            row_left = per;
-            next_codes += row_step;
-            next_scales += row_step;
+    // tiles are copied two at a time (the last of a row tile may be alone) in
+    // the order they are multiplied; a group of copies per step, empty ones
+    // after the last, so that the newest RING - 1 are always those ahead
+    uint32_t row_left = per, rows_left = per ? mine : 0u, slot_in = ring;
+    const uint64_t row_step = (stride * a.q.col_tiles - per) * TILE;
+    const uint8_t *src = a.packed + (rt0 * a.q.col_tiles + ct0 + lo) * TILE + 16u * lane;
+    auto next_slot = [&](uint32_t slot) {
+        return RING == 2u ? slot ^ ring ^ (ring + SLOT) : slot + SLOT == ring + RING * SLOT ? ring : slot + SLOT;
+    };
+    auto fetch = [&]() {
+        if (rows_left) {
+            const uint32_t bytes = row_left > 1u ? SLOT : TILE;
+#pragma unroll
+            for (uint32_t at = 0; at < SLOT; at += 512u)
+                if (at + 512u <= TILE || at + 16u * lane < bytes) cp_async16(slot_in + at + 16u * lane, src + at);
+            slot_in = next_slot(slot_in);
+            src += bytes;
+            row_left -= min(row_left, Q4_STEP);
+            if (row_left == 0u) {
+                row_left = per;
+                --rows_left;
+                src += row_step;
+            }
         }
+        cp_async_commit();
     };
 #pragma unroll
-    for (uint32_t u = 0; u < Q4_DEPTH; ++u) fetch(buf[u]);
+    for (uint32_t u = 0; u + 1u < RING; ++u) fetch();
 
     // the vectors' columns [128 ct0, 128 (ct0 + cts)), zeros past the matrix
     const uint32_t units = 16u * cts;
-    for (uint32_t i = threadIdx.x; i < units * a.m; i += 32u * Q4_WARPS) {
+    for (uint32_t i = threadIdx.x; i < units * a.m; i += 32u * W) {
         const uint32_t v = i / units, c = i % units, col = Q4_COLS * ct0 + 8u * c;
-        const uint16_t *src = a.x + v * a.ldx + col;
-        uint8_t *dst = smem + v * a.pitch + 16u * c;
+        const uint16_t *x = a.x + v * a.ldx + col;
+        uint8_t *dst = vecs + v * a.pitch + 16u * c;
         if (col >= a.q.cols) {
             *reinterpret_cast<uint4 *>(dst) = make_uint4(0u, 0u, 0u, 0u);
         } else if (a.xvec) {
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+            cp_async16(smem_u32(dst), x);
         } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) reinterpret_cast<uint16_t *>(dst)[j] = __ldg(src + j);
+            for (int j = 0; j < 8; ++j) reinterpret_cast<uint16_t *>(dst)[j] = __ldg(x + j);
         }
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
-    if (a.split > 1u) cluster_sync();  // (and the other CTAs run: their shared memory can be written)
+    cp_async_commit();
+    cp_async_wait<0>();
+    if constexpr (SPLIT) cluster_sync();  // (and the other CTAs run: their shared memory can be written)
     else __syncthreads();
 
-    const uint32_t x0 = smem_u32(smem) + min(g, a.m - 1u) * a.pitch + 16u * t;
+    const uint32_t x0 = smem_u32(vecs) + min(g, a.m - 1u) * a.pitch + 16u * t;
     const uint32_t nt_step = NT > 1 ? (min(g + 8u, a.m - 1u) - min(g, a.m - 1u)) * a.pitch : 0u;
     float acc[NT][4] = {};
-    uint32_t round = 0;
+    uint32_t round = 0, ct = lo, slot = ring;
 
-    // the end of a row tile: the group's sums, added in the warps' order
-    auto finish = [&]() {
-        float *p = part + (round & 1u) * Q4_WARPS * OUT + k * OUT;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {  // column-major: element (row, col) at 16 col + row
-            float *q = p + 128u * nt + 32u * t + g;
-            q[0] = acc[nt][0];
-            q[16] = acc[nt][1];
-            q[8] = acc[nt][2];
-            q[24] = acc[nt][3];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[nt][i] = 0.f;
-        }
+    auto group_barrier = [&]() {
         if (a.wk == 1u) __syncwarp();
-        else asm volatile("bar.sync %0, %1;" ::"r"(1u + group), "r"(32u * a.wk) : "memory");  // at most 8 groups
-        const float *r = part + (round & 1u) * Q4_WARPS * OUT;
-        const uint64_t rt = rt0 + round * stride;
-        for (uint32_t o = 32u * k + lane; o < 16u * a.m; o += 32u * a.wk) {
-            float v = r[o];
-            for (uint32_t w = 1; w < a.wk; ++w) v += r[w * OUT + o];
-            if (a.split == 1u) {
-                q4_store(a, Q4_ROWS * rt + (o & 15u), o >> 4, v);
-            } else {  // to the CTA of the cluster that adds this round's
-                const uint32_t slot = (round % a.batch / a.split * groups + group) * a.split + rank;
-                st_cluster_f32(map_rank(smem_u32(join + slot * 16u * a.m + o), round % a.split), v);
+        else asm volatile("bar.sync %0, %1;" ::"r"(group), "r"(32u * a.wk) : "memory");  // at most 16 groups
+    };
+    // The end of a row tile.  The warp puts its sums away; after `hold` row
+    // tiles (and the last) the group adds them up, in the warps' order.
+    auto finish = [&]() {
+        const uint32_t held = round % a.hold;
+        float *mysum = sums + (warp * a.hold + held) * outs;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint32_t col = 8u * nt + 2u * t + j;
+                if (col < a.m) {
+                    mysum[16u * col + g] = acc[nt][j];
+                    mysum[16u * col + g + 8u] = acc[nt][2 + j];
+                }
+                acc[nt][j] = acc[nt][2 + j] = 0.f;
             }
         }
         ++round;
-    };
-    // every `batch` rounds the cluster's CTAs add each other's sums, in order
-    auto meet = [&](uint32_t from) {
-        cluster_sync();
-        for (uint32_t i = threadIdx.x; i < a.batch / a.split * groups * 16u * a.m; i += 32u * Q4_WARPS) {
-            const uint32_t o = i % (16u * a.m), gr = i / (16u * a.m) % groups, rd = i / (16u * a.m) / groups * a.split + rank;
-            const uint64_t rt = (uint64_t)(blockIdx.x / a.split) * groups + gr + (from + rd) * stride;
-            if (from + rd >= a.rounds || rt >= a.q.row_tiles) continue;
-            const float *r = join + (rd / a.split * groups + gr) * a.split * 16u * a.m + o;
-            float v = r[0];
-            for (uint32_t w = 1; w < a.split; ++w) v += r[w * 16u * a.m];
-            q4_store(a, Q4_ROWS * rt + (o & 15u), o >> 4, v);
+        if (held + 1u < a.hold && round < mine) return;
+        group_barrier();
+        const float *r = sums + group * a.wk * a.hold * outs;
+        for (uint32_t i = 32u * k + lane; i < (held + 1u) * outs; i += 32u * a.wk) {
+            float v = r[i];
+            for (uint32_t w = 1; w < a.wk; ++w) v += r[w * a.hold * outs + i];
+            const uint32_t rd = round - 1u - held + i / outs, o = i % outs;
+            if constexpr (!SPLIT) {
+                q4_store(a, Q4_ROWS * (rt0 + rd * stride) + (o & 15u), o >> 4, v);
+            } else {  // to the CTA of the cluster that adds this round's
+                const uint32_t at = (rd % a.batch / split * groups + group) * split + rank;
+                st_cluster_f32(map_rank(smem_u32(join + at * outs + o), rd % split), v);
+            }
         }
-        cluster_sync();
+        group_barrier();  // before the next sums are put there
+    };
+    auto step = [&]() {
+        cp_async_wait<(int)RING - 2>();
+        __syncwarp();  // every lane's copies, and every lane is done with the slot that fetch() fills
+        fetch();
+        q4_tile_products<GT, Z, NT>(Q4Tile<GT, Z>(slot, lane), x0 + 256u * ct, nt_step, acc);
+        if (ct + 1u < hi) q4_tile_products<GT, Z, NT>(Q4Tile<GT, Z>(slot + TILE, lane), x0 + 256u * ct + 256u, nt_step, acc);
+        slot = next_slot(slot);
+        ct += Q4_STEP;
+        if (ct >= hi) {
+            ct = lo;
+            finish();
+        }
     };
 
-    if (a.split == 1u) {
-        uint32_t ct = lo;
-        for (uint32_t i = 0; i < total; i += Q4_DEPTH) {
-#pragma unroll
-            for (uint32_t u = 0; u < Q4_DEPTH; ++u) {
-                if (i + u >= total) break;
-                q4_tile_products<GT, Z, NT>(buf[u], x0 + 256u * ct, nt_step, acc);
-                fetch(buf[u]);
-                if (++ct == hi) {
-                    ct = lo;
-                    finish();
-                }
-            }
-        }
+    if constexpr (!SPLIT) {
         if (per == 0u)
             while (round < mine) finish();
-        return;
-    }
-    // in a cluster every group takes part in every meeting
-    uint32_t ct = lo, met = 0, i = 0;
-    while (met < a.rounds) {
-        const uint32_t until = min(met + a.batch, mine);
-        while (round < until) {
-            if (per == 0u) {
-                finish();
-                continue;
+        for (uint32_t i = mine * ((per + Q4_STEP - 1u) / Q4_STEP); i; --i) step();
+    } else {
+        // every `batch` rounds the cluster's CTAs add each other's sums, in
+        // order; every group takes part in every meeting
+        for (uint32_t met = 0; met < a.rounds; met += a.batch) {
+            const uint32_t until = min(met + a.batch, mine);
+            while (round < until) {
+                if (per) step();
+                else finish();
             }
-#pragma unroll
-            for (uint32_t u = 0; u < Q4_DEPTH; ++u) {
-                if (i % Q4_DEPTH != u || round >= until) continue;
-                q4_tile_products<GT, Z, NT>(buf[u], x0 + 256u * ct, nt_step, acc);
-                fetch(buf[u]);
-                ++i;
-                if (++ct == hi) {
-                    ct = lo;
-                    finish();
-                }
+            cluster_sync();
+            for (uint32_t i = threadIdx.x; i < a.batch / split * groups * outs; i += 32u * W) {
+                const uint32_t o = i % outs, gr = i / outs % groups, rd = i / outs / groups * split + rank;
+                const uint64_t rt = (uint64_t)(blockIdx.x / split) * groups + gr + (met + rd) * stride;
+                if (met + rd >= a.rounds || rt >= a.q.row_tiles) continue;
+                const float *r = join + (rd / split * groups + gr) * split * outs + o;
+                float v = r[0];
+                for (uint32_t w = 1; w < split; ++w) v += r[w * outs];
+                q4_store(a, Q4_ROWS * rt + (o & 15u), o >> 4, v);
             }
+            cluster_sync();
         }
-        meet(met);
-        met += a.batch;
     }
 }
 
@@ -614,12 +621,14 @@ namespace {
 // of one step are too small to be cut blindly: 4096 rows are 256 row tiles,
 // 1.7 per SM, and two of them in turn on some SMs would take as long as two on
 // all.
-void q4_cut(Q4GemvParams &a, uint32_t split, uint32_t ctas) {
+void q4_cut(Q4GemvParams &a, uint32_t split, uint32_t ctas, uint32_t warps) {
     a.split = split;
     a.tiles = (a.q.col_tiles + split - 1u) / split;
     uint64_t best = ~0ull;
-    for (uint32_t wk = 1; wk <= Q4_WARPS; wk *= 2u) {
-        const uint64_t at_once = (uint64_t)(ctas / split) * (Q4_WARPS / wk), rounds = (a.q.row_tiles + at_once - 1u) / at_once;
+    for (uint32_t wk = warps / 16u; wk <= warps; wk *= 2u) {  // at most 16 groups: named barriers
+        // (the sums of the cluster's groups have to fit their buffer)
+        if (split > 1u && warps / wk * split * 64u * a.m > Q4_JOIN_BYTES) continue;
+        const uint64_t at_once = (uint64_t)(ctas / split) * (warps / wk), rounds = (a.q.row_tiles + at_once - 1u) / at_once;
         const uint64_t cost = rounds * (2u * ((a.tiles + wk - 1u) / wk) + 1u);
         if (cost < best) {
             best = cost;
@@ -631,45 +640,50 @@ void q4_cut(Q4GemvParams &a, uint32_t split, uint32_t ctas) {
 
 typedef void (*q4_fn)(const Q4GemvParams);
 template <int GT, bool Z>
-q4_fn q4_variant(uint32_t m) {
-    return m > 8u ? q4_gemv_tiles<GT, Z, 2> : q4_gemv_tiles<GT, Z, 1>;
+q4_fn q4_variant(int nt, uint32_t warps, bool split) {
+    if (nt == 2) return split ? q4_gemv_tiles<GT, Z, 2, 16, true> : q4_gemv_tiles<GT, Z, 2, 16, false>;
+    if (warps == 16u) return split ? q4_gemv_tiles<GT, Z, 1, 16, true> : q4_gemv_tiles<GT, Z, 1, 16, false>;
+    return split ? q4_gemv_tiles<GT, Z, 1, 32, true> : q4_gemv_tiles<GT, Z, 1, 32, false>;
 }
-q4_fn q4_variant(const Q4Params &q, uint32_t m) {
+q4_fn q4_variant(const Q4Params &q, int nt, uint32_t warps, bool split) {
     switch (q.gt) {
-        case 1: return q.zeros ? q4_variant<1, true>(m) : q4_variant<1, false>(m);
-        case 2: return q.zeros ? q4_variant<2, true>(m) : q4_variant<2, false>(m);
-        default: return q.zeros ? q4_variant<4, true>(m) : q4_variant<4, false>(m);
+        case 1: return q.zeros ? q4_variant<1, true>(nt, warps, split) : q4_variant<1, false>(nt, warps, split);
+        case 2: return q.zeros ? q4_variant<2, true>(nt, warps, split) : q4_variant<2, false>(nt, warps, split);
+        default: return q.zeros ? q4_variant<4, true>(nt, warps, split) : q4_variant<4, false>(nt, warps, split);
     }
 }
 
 constexpr uint32_t SMEM_MOST = 227u * 1024u;
 
 dfw_status launch_q4_pass(Q4GemvParams a, int dev, int sms, cudaStream_t s) {
-    const q4_fn fn = q4_variant(a.q, a.m);
-    const uint32_t sums = 2u * Q4_WARPS * 128u * (a.m > 8u ? 2u : 1u) * 4u;
-    // as few CTAs to a row tile as their shared memory allows
-    uint32_t split = 1, x_bytes = 0;
-    for (;; split *= 2u) {
+    const int nt = a.m > 8u ? 2 : 1;
+    // as few CTAs to a row tile as their shared memory allows, then as many warps
+    uint32_t split = 1, warps = 0, smem = 0;
+    for (; split <= 8u && !warps; split *= 2u) {
         const uint32_t tiles = (a.q.col_tiles + split - 1u) / split;
         a.pitch = tiles * 2u * Q4_COLS + 64u;  // neighbouring vectors 16 banks apart
-        x_bytes = a.m * a.pitch;
-        if (x_bytes + sums + (split > 1u ? Q4_JOIN_BYTES : 0u) <= SMEM_MOST) break;
-        if (split == 8u) return DFW_EINVAL;  // (not reached: the caller bounds m by cols)
+        for (uint32_t w = nt == 1 ? 32u : 16u; w >= 16u && !warps; w -= 16u) {
+            smem = w * (q4_ring(nt, w) * Q4_STEP * a.q.tile_bytes + 64u * a.m) + a.m * a.pitch + (split > 1u ? Q4_JOIN_BYTES : 0u);
+            if (smem <= SMEM_MOST) warps = w;
+        }
     }
-    const uint32_t smem = x_bytes + sums + (split > 1u ? Q4_JOIN_BYTES : 0u);
-    static bool opted[16][12];
-    const uint32_t vi = (a.q.gt == 1u ? 0u : a.q.gt == 2u ? 1u : 2u) * 4u + a.q.zeros * 2u + (a.m > 8u ? 1u : 0u);
+    split /= 2u;
+    if (!warps) return DFW_EINVAL;  // (not reached: the caller bounds m by cols)
+    const q4_fn fn = q4_variant(a.q, nt, warps, split > 1u);
+    static bool opted[16][36];
+    const uint32_t vi = (a.q.gt == 1u ? 0u : a.q.gt == 2u ? 1u : 2u) * 12u + a.q.zeros * 6u + (nt == 2 ? 2u : warps == 16u ? 1u : 0u) * 2u + (split > 1u ? 1u : 0u);
     if (!opted[dev][vi]) {
         if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MOST) != cudaSuccess) return DFW_ECUDA;
         opted[dev][vi] = true;
     }
     uint32_t ctas = (uint32_t)sms;
     if (split > 1u) {  // clusters that find room at once: not every SM can be in one
-        static int room[16][9];
-        if (!room[dev][split]) {
+        static int room[16][2][9];  // by device, warps, cluster size (every variant fills an SM)
+        int &fit = room[dev][warps / 16u - 1u][split];
+        if (!fit) {
             cudaLaunchConfig_t cfg = {};
             cfg.gridDim = dim3(split);
-            cfg.blockDim = dim3(32u * Q4_WARPS);
+            cfg.blockDim = dim3(32u * warps);
             cfg.dynamicSmemBytes = SMEM_MOST;
             cudaLaunchAttribute attr[1];
             attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -679,16 +693,24 @@ dfw_status launch_q4_pass(Q4GemvParams a, int dev, int sms, cudaStream_t s) {
             cfg.numAttrs = 1;
             int n = 0;
             if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess || n < 1) return DFW_ECUDA;
-            room[dev][split] = n;
+            fit = n;
         }
-        ctas = (uint32_t)room[dev][split] * split;
+        ctas = (uint32_t)fit * split;
     }
-    q4_cut(a, split, ctas);
-    const uint32_t groups = Q4_WARPS / a.wk;
+    q4_cut(a, split, ctas, warps);
+    const uint32_t groups = warps / a.wk;
     const uint64_t clusters = std::min<uint64_t>(ctas / split, (a.q.row_tiles + groups - 1u) / groups);
-    a.batch = split;
-    while (a.batch < a.rounds && (a.batch / split + 1u) * groups * split * 16u * a.m * 4u <= Q4_JOIN_BYTES) a.batch += split;
-    return launch_with(fn, clusters * split, 32u * Q4_WARPS, smem, false, split, s, a);
+    // sums are added up every 8 row tiles if there is room to keep them
+    a.hold = 1u;
+    while (a.hold < 8u && a.hold < a.rounds && smem + warps * 64u * a.m * a.hold <= SMEM_MOST &&
+           (split == 1u || 2u * a.hold * groups * 64u * a.m <= Q4_JOIN_BYTES)) {
+        smem += warps * 64u * a.m * a.hold;
+        a.hold *= 2u;
+    }
+    const uint32_t unit = std::max(split, a.hold);  // both powers of two
+    a.batch = unit;
+    while (a.batch < a.rounds && ((a.batch + unit) / split) * groups * split * 64u * a.m <= Q4_JOIN_BYTES) a.batch += unit;
+    return launch_with(fn, clusters * split, 32u * warps, smem, false, split, s, a);
 }
 
 }  // namespace
@@ -712,7 +734,7 @@ dfw_status launch_q4_gemv(const uint8_t *d_packed, const dfw_q4_info *info, uint
     a.y_fp32 = (uint32_t)y_fp32;
     a.xvec = (reinterpret_cast<uintptr_t>(d_x) & 15u) == 0u && (m == 1u || ldx % 8u == 0u);
     // 16 vectors a pass, or 8 where 16 would not fit the eight CTAs of the largest cluster
-    const uint32_t most = a.q.col_tiles <= 272u ? 16u : 8u;
+    const uint32_t most = a.q.col_tiles <= 192u ? 16u : a.q.col_tiles <= 256u ? 8u : 4u;
     for (uint32_t j = 0; j < m; j += most) {
         a.m = std::min(most, m - j);
         a.x = d_x + j * ldx;
