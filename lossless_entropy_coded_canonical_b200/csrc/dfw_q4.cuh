@@ -257,7 +257,7 @@ struct Q4GemvParams {
     void *y;
     uint64_t ldx, ldy;
     uint32_t m, y_fp32;
-    uint32_t wk;       // warps along the columns of a row tile
+    uint32_t wk_log;   // log2 of the warps along the columns of a row tile
     uint32_t split;    // CTAs along them (the cluster)
     uint32_t tiles;    // column tiles per CTA
     uint32_t pitch;    // bytes from one vector to the next in shared memory
@@ -393,11 +393,11 @@ __global__ void __launch_bounds__(32 * W, 1) q4_gemv_tiles(const Q4GemvParams a)
     const uint32_t outs = 16u * a.m;  // sums of a row tile, column by column
     const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3u;
     const uint32_t split = SPLIT ? a.split : 1u, rank = blockIdx.x % split;
-    const uint32_t group = warp / a.wk, k = warp % a.wk, groups = W / a.wk;
+    const uint32_t wk = 1u << a.wk_log, group = warp >> a.wk_log, k = warp & (wk - 1u), groups = W >> a.wk_log;
     const uint32_t ct0 = rank * a.tiles, cts = ct0 < a.q.col_tiles ? min(a.tiles, a.q.col_tiles - ct0) : 0u;
-    const uint32_t lo = k * cts / a.wk, hi = (k + 1u) * cts / a.wk, per = hi - lo;  // this warp's column tiles, from ct0
+    const uint32_t lo = (k * cts) >> a.wk_log, hi = ((k + 1u) * cts) >> a.wk_log, per = hi - lo;  // this warp's column tiles, from ct0
     const uint64_t rt0 = (uint64_t)(blockIdx.x / split) * groups + group, stride = (uint64_t)(gridDim.x / split) * groups;
-    const uint32_t mine = rt0 < a.q.row_tiles ? (uint32_t)((a.q.row_tiles - 1u - rt0) / stride) + 1u : 0u;  // row tiles
+    const uint32_t mine = a.rounds - (rt0 + (a.rounds - 1u) * stride < a.q.row_tiles ? 0u : 1u);  // row tiles
     const uint32_t ring = smem_u32(smem) + warp * RING * SLOT;
     float *sums = reinterpret_cast<float *>(smem + W * RING * SLOT);
     uint8_t *vecs = reinterpret_cast<uint8_t *>(sums + W * a.hold * outs);
@@ -433,18 +433,19 @@ __global__ void __launch_bounds__(32 * W, 1) q4_gemv_tiles(const Q4GemvParams a)
     for (uint32_t u = 0; u + 1u < RING; ++u) fetch();
 
     // the vectors' columns [128 ct0, 128 (ct0 + cts)), zeros past the matrix
-    const uint32_t units = 16u * cts;
-    for (uint32_t i = threadIdx.x; i < units * a.m; i += 32u * W) {
-        const uint32_t v = i / units, c = i % units, col = Q4_COLS * ct0 + 8u * c;
-        const uint16_t *x = a.x + v * a.ldx + col;
-        uint8_t *dst = vecs + v * a.pitch + 16u * c;
-        if (col >= a.q.cols) {
-            *reinterpret_cast<uint4 *>(dst) = make_uint4(0u, 0u, 0u, 0u);
-        } else if (a.xvec) {
-            cp_async16(smem_u32(dst), x);
-        } else {
+    for (uint32_t v = 0; v < a.m; ++v) {
+        for (uint32_t c = threadIdx.x; c < 16u * cts; c += 32u * W) {
+            const uint32_t col = Q4_COLS * ct0 + 8u * c;
+            const uint16_t *x = a.x + v * a.ldx + col;
+            uint8_t *dst = vecs + v * a.pitch + 16u * c;
+            if (col >= a.q.cols) {
+                *reinterpret_cast<uint4 *>(dst) = make_uint4(0u, 0u, 0u, 0u);
+            } else if (a.xvec) {
+                cp_async16(smem_u32(dst), x);
+            } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) reinterpret_cast<uint16_t *>(dst)[j] = __ldg(x + j);
+                for (int j = 0; j < 8; ++j) reinterpret_cast<uint16_t *>(dst)[j] = __ldg(x + j);
+            }
         }
     }
     cp_async_commit();
@@ -458,8 +459,8 @@ __global__ void __launch_bounds__(32 * W, 1) q4_gemv_tiles(const Q4GemvParams a)
     uint32_t round = 0, ct = lo, slot = ring;
 
     auto group_barrier = [&]() {
-        if (a.wk == 1u) __syncwarp();
-        else asm volatile("bar.sync %0, %1;" ::"r"(group), "r"(32u * a.wk) : "memory");  // at most 16 groups
+        if (wk == 1u) __syncwarp();
+        else asm volatile("bar.sync %0, %1;" ::"r"(group), "r"(32u * wk) : "memory");  // at most 16 groups
     };
     // The end of a row tile.  The warp puts its sums away; after `hold` row
     // tiles (and the last) the group adds them up, in the warps' order.
@@ -481,10 +482,11 @@ __global__ void __launch_bounds__(32 * W, 1) q4_gemv_tiles(const Q4GemvParams a)
         ++round;
         if (held + 1u < a.hold && round < mine) return;
         group_barrier();
-        const float *r = sums + group * a.wk * a.hold * outs;
-        for (uint32_t i = 32u * k + lane; i < (held + 1u) * outs; i += 32u * a.wk) {
+        const float *r = sums + group * wk * a.hold * outs;
+        for (uint32_t i = 32u * k + lane; i < (held + 1u) * outs; i += 32u * wk) {
             float v = r[i];
-            for (uint32_t w = 1; w < a.wk; ++w) v += r[w * a.hold * outs + i];
+#pragma unroll 8
+            for (uint32_t w = 1; w < wk; ++w) v += r[w * a.hold * outs + i];
             const uint32_t rd = round - 1u - held + i / outs, o = i % outs;
             if constexpr (!SPLIT) {
                 q4_store(a, Q4_ROWS * (rt0 + rd * stride) + (o & 15u), o >> 4, v);
@@ -625,14 +627,15 @@ void q4_cut(Q4GemvParams &a, uint32_t split, uint32_t ctas, uint32_t warps) {
     a.split = split;
     a.tiles = (a.q.col_tiles + split - 1u) / split;
     uint64_t best = ~0ull;
-    for (uint32_t wk = warps / 16u; wk <= warps; wk *= 2u) {  // at most 16 groups: named barriers
+    for (uint32_t log = warps / 32u; (1u << log) <= warps; ++log) {  // at most 16 groups: named barriers
+        const uint32_t wk = 1u << log;
         // (the sums of the cluster's groups have to fit their buffer)
         if (split > 1u && warps / wk * split * 64u * a.m > Q4_JOIN_BYTES) continue;
         const uint64_t at_once = (uint64_t)(ctas / split) * (warps / wk), rounds = (a.q.row_tiles + at_once - 1u) / at_once;
         const uint64_t cost = rounds * (2u * ((a.tiles + wk - 1u) / wk) + 1u);
         if (cost < best) {
             best = cost;
-            a.wk = wk;
+            a.wk_log = log;
             a.rounds = (uint32_t)rounds;
         }
     }
@@ -698,7 +701,7 @@ dfw_status launch_q4_pass(Q4GemvParams a, int dev, int sms, cudaStream_t s) {
         ctas = (uint32_t)fit * split;
     }
     q4_cut(a, split, ctas, warps);
-    const uint32_t groups = warps / a.wk;
+    const uint32_t groups = warps >> a.wk_log;
     const uint64_t clusters = std::min<uint64_t>(ctas / split, (a.q.row_tiles + groups - 1u) / groups);
     // sums are added up every 8 row tiles if there is room to keep them
     a.hold = 1u;
