@@ -238,16 +238,19 @@ __global__ void __launch_bounds__(256) q4_dequantise_tiles(const uint8_t *__rest
 // multiplies the sum (a bf16 weight s (q - z) would round); the 64 multiplies
 // the finished sum.
 //
-// A warp walks tiles along the columns, the next ones on their way into its
-// ring of tiles in shared memory (asynchronous copies: tiles in flight in
-// registers left room for half the warps).  WK warps share a row tile's columns
-// and add their sums through shared memory in a fixed order, W / WK row tiles
-// side by side in a CTA of W warps; when the vectors are too long for one SM's
-// shared memory a cluster of 2 to 8 CTAs shares the columns the same way.
+// A CTA takes consecutive row tiles, `pass` of them at a time, and its warps
+// take equal runs of their tiles, whichever rows they fall in (giving each
+// warp, or each few warps, whole row tiles left them unequal: 28672 rows are
+// 12.1 row tiles per SM).  The next two tiles are on their way into the warp's
+// ring in shared memory (asynchronous copies: tiles in flight in registers
+// left room for half the warps).  A warp leaves its sums of each row tile it
+// touched in shared memory; at the end of the pass they are added in the
+// warps' order.  When the vectors are too long for one SM's shared memory, a
+// cluster of 2 to 8 CTAs shares the columns and joins its sums the same way.
 // Up to 8 vectors take 32 warps of 64 registers, or 16 where their shared
 // memory does not allow 32; 9 to 16 have twice the sums and take 16.
-constexpr uint32_t Q4_STEP = 2;                          // tiles a warp takes at a time
-constexpr uint32_t Q4_JOIN_BYTES = 16u * 1024u;          // a CTA's buffer for its cluster's sums
+constexpr uint32_t Q4_STEP = 2;                   // tiles a warp takes at a time
+constexpr uint32_t Q4_JOIN_BYTES = 16u * 1024u;   // a CTA's buffer for its cluster's sums
 __host__ __device__ constexpr uint32_t q4_ring(int nt, uint32_t warps) { return nt == 1 && warps == 16u ? 3u : 2u; }  // steps in a warp's ring
 
 struct Q4GemvParams {
@@ -257,13 +260,11 @@ struct Q4GemvParams {
     void *y;
     uint64_t ldx, ldy;
     uint32_t m, y_fp32;
-    uint32_t wk_log;   // log2 of the warps along the columns of a row tile
-    uint32_t split;    // CTAs along them (the cluster)
+    uint32_t split;    // CTAs along the columns (the cluster)
     uint32_t tiles;    // column tiles per CTA
     uint32_t pitch;    // bytes from one vector to the next in shared memory
-    uint32_t rounds;   // row tiles per group of wk warps
-    uint32_t hold;     // row tiles a warp keeps its sums of before the group adds them up
-    uint32_t batch;    // rounds between two joins of the cluster's sums (a multiple of hold)
+    uint32_t pass;     // row tiles between two joins of the warps' sums
+    uint32_t share, extra;  // row tiles per cluster, and how many clusters take one more
     uint32_t xvec;     // the vectors can be read 16 bytes at a time
 };
 
@@ -384,49 +385,56 @@ __device__ __forceinline__ void q4_store(const Q4GemvParams &a, uint64_t row, ui
     else static_cast<__nv_bfloat16 *>(a.y)[col * a.ldy + row] = __float2bfloat16_rn(v);
 }
 
-// Shared memory: the warps' rings | the warps' sums | the vectors | [clusters]
-// the sums of the cluster's CTAs.
+// Shared memory: the warps' rings | the sums of (warp, row tile), at index
+// warp + row tile of the pass: in the order of the tiles each next pair has a
+// larger one | the vectors | [clusters] the sums of the cluster's CTAs.
 template <int GT, bool Z, int NT, uint32_t W, bool SPLIT>
 __global__ void __launch_bounds__(32 * W, 1) q4_gemv_tiles(const Q4GemvParams a) {
     extern __shared__ __align__(16) uint8_t smem[];
     constexpr uint32_t TILE = Q4_CODES + 32u * GT + (Z ? 16u * GT : 0u), SLOT = Q4_STEP * TILE, RING = q4_ring(NT, W);
     const uint32_t outs = 16u * a.m;  // sums of a row tile, column by column
     const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3u;
-    const uint32_t split = SPLIT ? a.split : 1u, rank = blockIdx.x % split;
-    const uint32_t wk = 1u << a.wk_log, group = warp >> a.wk_log, k = warp & (wk - 1u), groups = W >> a.wk_log;
+    const uint32_t split = SPLIT ? a.split : 1u, rank = blockIdx.x % split, me = blockIdx.x / split;
     const uint32_t ct0 = rank * a.tiles, cts = ct0 < a.q.col_tiles ? min(a.tiles, a.q.col_tiles - ct0) : 0u;
-    const uint32_t lo = (k * cts) >> a.wk_log, hi = ((k + 1u) * cts) >> a.wk_log, per = hi - lo;  // this warp's column tiles, from ct0
-    const uint64_t rt0 = (uint64_t)(blockIdx.x / split) * groups + group, stride = (uint64_t)(gridDim.x / split) * groups;
-    const uint32_t mine = a.rounds - (rt0 + (a.rounds - 1u) * stride < a.q.row_tiles ? 0u : 1u);  // row tiles
+    const uint32_t rt0 = me * a.share + min(me, a.extra), rows = a.share + (me < a.extra ? 1u : 0u);  // row tiles
     const uint32_t ring = smem_u32(smem) + warp * RING * SLOT;
     float *sums = reinterpret_cast<float *>(smem + W * RING * SLOT);
-    uint8_t *vecs = reinterpret_cast<uint8_t *>(sums + W * a.hold * outs);
+    uint8_t *vecs = reinterpret_cast<uint8_t *>(sums + (W + a.pass - 1u) * outs);
     float *join = reinterpret_cast<float *>(vecs + a.m * a.pitch);
+    // this warp's tiles of a pass over `n` row tiles: [first(warp), first(warp + 1))
+    auto first = [&](uint32_t w, uint32_t n) { return w * (n * cts) / W; };
 
-    // tiles are copied two at a time (the last of a row tile may be alone) in
-    // the order they are multiplied; a group of copies per step, empty ones
-    // after the last, so that the newest RING - 1 are always those ahead
-    uint32_t row_left = per, rows_left = per ? mine : 0u, slot_in = ring;
-    const uint64_t row_step = (stride * a.q.col_tiles - per) * TILE;
-    const uint8_t *src = a.packed + (rt0 * a.q.col_tiles + ct0 + lo) * TILE + 16u * lane;
+    // tiles are copied in the order they are multiplied, a group of copies per
+    // step (empty ones after the last, so that the newest RING - 1 groups are
+    // always those ahead)
+    uint32_t in_row = 0, in_left = 0, in_ct = 0, slot_in = ring;
+    const uint8_t *src = nullptr;
     auto next_slot = [&](uint32_t slot) {
         return RING == 2u ? slot ^ ring ^ (ring + SLOT) : slot + SLOT == ring + RING * SLOT ? ring : slot + SLOT;
     };
     auto fetch = [&]() {
-        if (rows_left) {
-            const uint32_t bytes = row_left > 1u ? SLOT : TILE;
-#pragma unroll
-            for (uint32_t at = 0; at < SLOT; at += 512u)
-                if (at + 512u <= TILE || at + 16u * lane < bytes) cp_async16(slot_in + at + 16u * lane, src + at);
-            slot_in = next_slot(slot_in);
-            src += bytes;
-            row_left -= min(row_left, Q4_STEP);
-            if (row_left == 0u) {
-                row_left = per;
-                --rows_left;
-                src += row_step;
-            }
+        while (in_left == 0u && in_row < rows && cts) {  // the next pass
+            const uint32_t n = min(a.pass, rows - in_row), lo = first(warp, n);
+            in_left = first(warp + 1u, n) - lo;
+            in_ct = lo % cts;
+            src = a.packed + ((uint64_t)(rt0 + in_row + lo / cts) * a.q.col_tiles + ct0 + in_ct) * TILE + 16u * lane;
+            in_row += n;
         }
+#pragma unroll
+        for (uint32_t u = 0; u < Q4_STEP; ++u) {
+            if (in_left == 0u) break;
+            const uint32_t dst = slot_in + u * TILE + 16u * lane;
+            cp_async16(dst, src);
+            cp_async16(dst + 512u, src + 512);
+            if (lane < (TILE - Q4_CODES) / 16u) cp_async16(dst + Q4_CODES, src + Q4_CODES);
+            src += TILE;
+            if (SPLIT && ++in_ct == cts) {
+                in_ct = 0;
+                src += (uint64_t)(a.q.col_tiles - cts) * TILE;
+            }
+            --in_left;
+        }
+        slot_in = next_slot(slot_in);
         cp_async_commit();
     };
 #pragma unroll
@@ -456,85 +464,68 @@ __global__ void __launch_bounds__(32 * W, 1) q4_gemv_tiles(const Q4GemvParams a)
     const uint32_t x0 = smem_u32(vecs) + min(g, a.m - 1u) * a.pitch + 16u * t;
     const uint32_t nt_step = NT > 1 ? (min(g + 8u, a.m - 1u) - min(g, a.m - 1u)) * a.pitch : 0u;
     float acc[NT][4] = {};
-    uint32_t round = 0, ct = lo, slot = ring;
-
-    auto group_barrier = [&]() {
-        if (wk == 1u) __syncwarp();
-        else asm volatile("bar.sync %0, %1;" ::"r"(group), "r"(32u * wk) : "memory");  // at most 16 groups
-    };
-    // The end of a row tile.  The warp puts its sums away; after `hold` row
-    // tiles (and the last) the group adds them up, in the warps' order.
-    auto finish = [&]() {
-        const uint32_t held = round % a.hold;
-        float *mysum = sums + (warp * a.hold + held) * outs;
+    uint32_t slot = ring;
+    auto put_away = [&](uint32_t row) {
+        float *p = sums + (warp + row) * outs;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const uint32_t col = 8u * nt + 2u * t + j;
                 if (col < a.m) {
-                    mysum[16u * col + g] = acc[nt][j];
-                    mysum[16u * col + g + 8u] = acc[nt][2 + j];
+                    p[16u * col + g] = acc[nt][j];
+                    p[16u * col + g + 8u] = acc[nt][2 + j];
                 }
                 acc[nt][j] = acc[nt][2 + j] = 0.f;
             }
         }
-        ++round;
-        if (held + 1u < a.hold && round < mine) return;
-        group_barrier();
-        const float *r = sums + group * wk * a.hold * outs;
-        for (uint32_t i = 32u * k + lane; i < (held + 1u) * outs; i += 32u * wk) {
-            float v = r[i];
-#pragma unroll 8
-            for (uint32_t w = 1; w < wk; ++w) v += r[w * a.hold * outs + i];
-            const uint32_t rd = round - 1u - held + i / outs, o = i % outs;
-            if constexpr (!SPLIT) {
-                q4_store(a, Q4_ROWS * (rt0 + rd * stride) + (o & 15u), o >> 4, v);
-            } else {  // to the CTA of the cluster that adds this round's
-                const uint32_t at = (rd % a.batch / split * groups + group) * split + rank;
-                st_cluster_f32(map_rank(smem_u32(join + at * outs + o), rd % split), v);
-            }
-        }
-        group_barrier();  // before the next sums are put there
-    };
-    auto step = [&]() {
-        cp_async_wait<(int)RING - 2>();
-        __syncwarp();  // every lane's copies, and every lane is done with the slot that fetch() fills
-        fetch();
-        q4_tile_products<GT, Z, NT>(Q4Tile<GT, Z>(slot, lane), x0 + 256u * ct, nt_step, acc);
-        if (ct + 1u < hi) q4_tile_products<GT, Z, NT>(Q4Tile<GT, Z>(slot + TILE, lane), x0 + 256u * ct + 256u, nt_step, acc);
-        slot = next_slot(slot);
-        ct += Q4_STEP;
-        if (ct >= hi) {
-            ct = lo;
-            finish();
-        }
     };
 
-    if constexpr (!SPLIT) {
-        if (per == 0u)
-            while (round < mine) finish();
-        for (uint32_t i = mine * ((per + Q4_STEP - 1u) / Q4_STEP); i; --i) step();
-    } else {
-        // every `batch` rounds the cluster's CTAs add each other's sums, in
-        // order; every group takes part in every meeting
-        for (uint32_t met = 0; met < a.rounds; met += a.batch) {
-            const uint32_t until = min(met + a.batch, mine);
-            while (round < until) {
-                if (per) step();
-                else finish();
+    for (uint32_t done = 0; done < rows; done += a.pass) {
+        const uint32_t n = min(a.pass, rows - done), lo = first(warp, n), hi = first(warp + 1u, n);
+        uint32_t row = cts ? lo / cts : 0u, ct = lo - row * cts;
+        for (uint32_t i = lo; i < hi; i += Q4_STEP) {
+            cp_async_wait<(int)RING - 2>();
+            __syncwarp();  // every lane's copies, and every lane is done with the slot that fetch() fills
+            fetch();
+#pragma unroll
+            for (uint32_t u = 0; u < Q4_STEP; ++u) {
+                if (i + u >= hi) break;
+                q4_tile_products<GT, Z, NT>(Q4Tile<GT, Z>(slot + u * TILE, lane), x0 + 256u * ct, nt_step, acc);
+                if (++ct == cts) {
+                    put_away(row++);
+                    ct = 0;
+                }
+            }
+            slot = next_slot(slot);
+        }
+        if (ct || lo == hi) put_away(row);  // (a warp without tiles puts zeros between its neighbours' sums)
+        __syncthreads();
+        for (uint32_t i = threadIdx.x; i < n * outs; i += 32u * W) {
+            const uint32_t r = i / outs, o = i - r * outs;
+            // the warps whose runs meet tiles [r cts, (r + 1) cts): from the first that ends behind r cts
+            float v = 0.f;
+            if (cts) {
+                const uint32_t tiles = n * cts, w0 = ((r * cts + 1u) * W + tiles - 1u) / tiles - 1u;
+                const uint32_t w1 = ((r + 1u) * cts * W + tiles - 1u) / tiles;
+#pragma unroll 8
+                for (uint32_t w = w0; w < w1; ++w) v += sums[(w + r) * outs + o];
+            }
+            if constexpr (!SPLIT) q4_store(a, (uint64_t)Q4_ROWS * (rt0 + done + r) + (o & 15u), o >> 4, v);
+            else st_cluster_f32(map_rank(smem_u32(join + ((r / split) * split + rank) * outs + o), r % split), v);
+        }
+        if constexpr (SPLIT) {  // row tile r of the pass is added up by CTA r mod split
+            cluster_sync();
+            for (uint32_t i = threadIdx.x; rank + i / outs * split < n; i += 32u * W) {
+                const uint32_t r = rank + i / outs * split, o = i % outs;
+                const float *p = join + (r / split) * split * outs + o;
+                float v = p[0];
+                for (uint32_t w = 1; w < split; ++w) v += p[w * outs];
+                q4_store(a, (uint64_t)Q4_ROWS * (rt0 + done + r) + (o & 15u), o >> 4, v);
             }
             cluster_sync();
-            for (uint32_t i = threadIdx.x; i < a.batch / split * groups * outs; i += 32u * W) {
-                const uint32_t o = i % outs, gr = i / outs % groups, rd = i / outs / groups * split + rank;
-                const uint64_t rt = (uint64_t)(blockIdx.x / split) * groups + gr + (met + rd) * stride;
-                if (met + rd >= a.rounds || rt >= a.q.row_tiles) continue;
-                const float *r = join + (rd / split * groups + gr) * split * outs + o;
-                float v = r[0];
-                for (uint32_t w = 1; w < split; ++w) v += r[w * outs];
-                q4_store(a, Q4_ROWS * rt + (o & 15u), o >> 4, v);
-            }
-            cluster_sync();
+        } else {
+            __syncthreads();
         }
     }
 }
@@ -618,29 +609,6 @@ dfw_status launch_q4_dequantise(const uint8_t *d_packed, const dfw_q4_info *info
 
 namespace {
 
-// How a product is cut: wk and split by the time they give, counted in tiles
-// a warp walks (a row tile's sums cost about half a tile more).  The matrices
-// of one step are too small to be cut blindly: 4096 rows are 256 row tiles,
-// 1.7 per SM, and two of them in turn on some SMs would take as long as two on
-// all.
-void q4_cut(Q4GemvParams &a, uint32_t split, uint32_t ctas, uint32_t warps) {
-    a.split = split;
-    a.tiles = (a.q.col_tiles + split - 1u) / split;
-    uint64_t best = ~0ull;
-    for (uint32_t log = warps / 32u; (1u << log) <= warps; ++log) {  // at most 16 groups: named barriers
-        const uint32_t wk = 1u << log;
-        // (the sums of the cluster's groups have to fit their buffer)
-        if (split > 1u && warps / wk * split * 64u * a.m > Q4_JOIN_BYTES) continue;
-        const uint64_t at_once = (uint64_t)(ctas / split) * (warps / wk), rounds = (a.q.row_tiles + at_once - 1u) / at_once;
-        const uint64_t cost = rounds * (2u * ((a.tiles + wk - 1u) / wk) + 1u);
-        if (cost < best) {
-            best = cost;
-            a.wk_log = log;
-            a.rounds = (uint32_t)rounds;
-        }
-    }
-}
-
 typedef void (*q4_fn)(const Q4GemvParams);
 template <int GT, bool Z>
 q4_fn q4_variant(int nt, uint32_t warps, bool split) {
@@ -700,19 +668,17 @@ dfw_status launch_q4_pass(Q4GemvParams a, int dev, int sms, cudaStream_t s) {
         }
         ctas = (uint32_t)fit * split;
     }
-    q4_cut(a, split, ctas, warps);
-    const uint32_t groups = warps >> a.wk_log;
-    const uint64_t clusters = std::min<uint64_t>(ctas / split, (a.q.row_tiles + groups - 1u) / groups);
-    // sums are added up every 8 row tiles if there is room to keep them
-    a.hold = 1u;
-    while (a.hold < 8u && a.hold < a.rounds && smem + warps * 64u * a.m * a.hold <= SMEM_MOST &&
-           (split == 1u || 2u * a.hold * groups * 64u * a.m <= Q4_JOIN_BYTES)) {
-        smem += warps * 64u * a.m * a.hold;
-        a.hold *= 2u;
-    }
-    const uint32_t unit = std::max(split, a.hold);  // both powers of two
-    a.batch = unit;
-    while (a.batch < a.rounds && ((a.batch + unit) / split) * groups * split * 64u * a.m <= Q4_JOIN_BYTES) a.batch += unit;
+    a.split = split;
+    a.tiles = (a.q.col_tiles + split - 1u) / split;
+    const uint64_t clusters = std::min<uint64_t>(ctas / split, a.q.row_tiles);
+    // as many row tiles to a pass as there is room for their sums
+    const uint64_t rows = (a.q.row_tiles + clusters - 1u) / clusters;
+    uint64_t room = 1u + (SMEM_MOST - smem) / (64u * a.m);
+    if (split > 1u) room = std::min<uint64_t>(room, Q4_JOIN_BYTES / (64u * a.m) / split * split);
+    a.pass = (uint32_t)std::min(rows, room);
+    a.share = (uint32_t)(a.q.row_tiles / clusters);
+    a.extra = (uint32_t)(a.q.row_tiles % clusters);
+    smem += (a.pass - 1u) * 64u * a.m;
     return launch_with(fn, clusters * split, 32u * warps, smem, false, split, s, a);
 }
 
