@@ -42,12 +42,19 @@ __device__ __forceinline__ bool token_row(const IdSource &s, uint32_t t, uint64_
     return true;
 }
 
-// bf16(scale w), rounded to nearest even; scale 1 keeps the bits (NaN
-// payloads included), as the decoder does.
-__device__ __forceinline__ uint16_t scaled(uint16_t w, float scale, bool one) {
+// Two bf16(scale w), each rounded to nearest even; scale 1 keeps the bits
+// (NaN payloads included), as the decoder does.
+__device__ __forceinline__ uint32_t scaled2(uint32_t w, float scale, bool one) {
     if (one) return w;
-    return __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float((uint32_t)w << 16) * scale));
+    const float lo = __uint_as_float(w << 16) * scale, hi = __uint_as_float(w & 0xFFFF0000u) * scale;
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
 }
+__device__ __forceinline__ uint4 scaled8(uint4 w, float scale, bool one) {
+    return make_uint4(scaled2(w.x, scale, one), scaled2(w.y, scale, one), scaled2(w.z, scale, one), scaled2(w.w, scale, one));
+}
+__device__ __forceinline__ uint16_t scaled1(uint32_t w, float scale, bool one) { return (uint16_t)scaled2(w, scale, one); }
 
 // ------------------------------------------------------- rows of a bf16 table
 
@@ -56,18 +63,42 @@ struct RowsOfTable {
     const uint16_t *table;
     uint16_t *out;
     uint64_t ldt, ldo;
-    uint32_t dim;
+    uint32_t dim, parts;  // parts: pieces of EMBED_PART a row is cut into
     float scale;
 };
 
+// A warp copies one piece of a row: VEC weights per lane and access, four
+// accesses in flight.
+constexpr uint32_t EMBED_PART = 1024;
+
+template <int VEC>
 __global__ void __launch_bounds__(256) embed_table_rows(const RowsOfTable p) {
     const bool one = p.scale == 1.f;
     const uint32_t lane = threadIdx.x & 31u;
-    for (uint32_t t = blockIdx.x * 8u + (threadIdx.x >> 5); t < p.ids.tokens; t += gridDim.x * 8u) {
-        uint64_t row = 0;
-        const bool have = token_row(p.ids, t, row, lane == 0u);
-        for (uint32_t c = lane; c < p.dim; c += 32u)
-            p.out[t * p.ldo + c] = have ? scaled(__ldg(p.table + row * p.ldt + c), p.scale, one) : (uint16_t)0;
+    const uint64_t piece = blockIdx.x * 8ull + (threadIdx.x >> 5);
+    const uint32_t t = (uint32_t)(piece / p.parts), c0 = (uint32_t)(piece % p.parts) * EMBED_PART;
+    if (t >= p.ids.tokens) return;
+    uint64_t row = 0;
+    const bool have = token_row(p.ids, t, row, lane == 0u);
+    const uint16_t *src = p.table + row * p.ldt;
+    uint16_t *dst = p.out + t * p.ldo;
+    const uint32_t end = min(p.dim, c0 + EMBED_PART);
+    if constexpr (VEC == 8) {
+        uint4 v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t c = c0 + 256u * i + 8u * lane;
+            v[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (have && c < end) v[i] = __ldg(reinterpret_cast<const uint4 *>(src + c));
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t c = c0 + 256u * i + 8u * lane;
+            if (c < end) __stcs(reinterpret_cast<uint4 *>(dst + c), scaled8(v[i], p.scale, one));
+        }
+    } else {
+#pragma unroll 8
+        for (uint32_t c = c0 + lane; c < end; c += 32u) dst[c] = have ? scaled1(__ldg(src + c), p.scale, one) : (uint16_t)0;
     }
 }
 
@@ -80,99 +111,263 @@ struct RowsOfLanes {
     uint64_t total_bits;
     uint16_t *out;
     uint64_t ldo;
-    uint32_t dim, row_groups;  // groups a row can touch
+    uint32_t dim;
+    uint32_t units;        // units a token's row is cut into: its groups if rows are whole groups or parts of one, else 1
     uint32_t single;       // total_bits == 0: every exponent is this one
     float scale;
 };
 
-// One warp per (token, group the row touches); each lane decodes its chunk of
-// the group if the row needs it, one codeword per lookup of the byte-keyed
-// table 0 (1 KB of shared memory).
-__global__ void __launch_bounds__(128) embed_lanes_rows(const RowsOfLanes p) {
-    __shared__ uint32_t s_root[256];
-    __shared__ uint32_t s_exp[4][16 * 32];  // word k of lane l's chunk at 32 k + l
-    const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
-    const uint32_t *hier = p.lanes.lut + (2u << p.lanes.fast_bits);
-    if (p.total_bits)
-        for (uint32_t i = threadIdx.x; i < 256u; i += 128u) s_root[i] = __ldg(hier + i);
-    __syncthreads();
+// Writes zeros to weights [c0, c1) of a token's row.
+__device__ __forceinline__ void zero_row(uint16_t *out, uint32_t c0, uint32_t c1, uint32_t lane) {
+    for (uint32_t c = c0 + lane; c < c1; c += 32u) out[c] = 0;
+}
+
+// The decode kernel's work on chosen groups: a warp takes the groups of a
+// token's row in turn (in units of a group where every row is whole groups or
+// lies in one), staged as decode_lanes stages its own (the same copies,
+// positions, lookups and checks), except that lanes whose chunk the row does
+// not touch decode nothing, and the join scales and writes the row's part of
+// the group.  The id of the unit after the next and the starts of the group
+// after the current one are loaded ahead.  Few tokens take small CTAs, one
+// group per warp: the table copy and its check then overlap the first group's
+// three dependent loads (id, group start, stream).
+// V: the join's weights per access; every row begins at a multiple of V in
+// the scope and at 2 V bytes in the output (V = 1: no alignment).
+template <int NT, int V>
+__global__ void __launch_bounds__(NT) embed_lanes_rows(const RowsOfLanes p) {
+    constexpr uint32_t NWARP = NT / 32;
+    extern __shared__ __align__(16) uint8_t smem[];
+    const LanesParams &prm = p.lanes;
+    const uint32_t n_fast = 1u << prm.fast_bits;
+    uint2 *s_fast = reinterpret_cast<uint2 *>(smem);
+    const uint32_t wbytes = warp_smem_bytes(prm.sbuf_bytes);
+    const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
+    uint8_t *wbase = smem + (8u << prm.fast_bits) + warp * wbytes;
+    const uint32_t bar_s0 = smem_u32(wbase), bar_m = bar_s0 + 16u, bar_t = smem_u32(smem + (8u << prm.fast_bits)) + 24u;
+    uint8_t *wslots = wbase + 32;
+    const uint32_t slot_bytes = 64u + prm.sbuf_bytes;
+    uint8_t *mbuf = wslots + 2u * slot_bytes;
+    const uint32_t exps0 = smem_u32(mbuf + GROUP_SYMS), exps = exps0 + 4u * lane;
+    const uint32_t *g_hier = prm.lut + 2u * n_fast;
+    const uint32_t kshift = 32u - prm.fast_bits;
     const bool one = p.scale == 1.f;
-    const uint64_t items = (uint64_t)p.ids.tokens * p.row_groups;
-    for (uint64_t item = blockIdx.x * 4ull + warp; item < items; item += gridDim.x * 4ull) {
-        const uint32_t t = (uint32_t)(item / p.row_groups);
+
+    if (lane == 0u) {
+        mbar_init(bar_s0, 1);
+        mbar_init(bar_s0 + 8u, 1);
+        mbar_init(bar_m, 1);
+        if (tid == 0u) mbar_init(bar_t, 1);
+        fence_mbar_init();
+        if (tid == 0u) {
+            mbar_expect_tx(bar_t, 8u << prm.fast_bits);
+            bulk_load(smem_u32(s_fast), prm.lut, 8u << prm.fast_bits, bar_t);
+        }
+    }
+
+    // a group of a token's row
+    struct Item {
+        uint64_t w0;          // the row's first weight
+        uint64_t s0, s1;      // the group's bits
+        uint32_t t, g, last;  // token, group, the unit's last group
+    };
+    const uint32_t n_units = p.ids.tokens * p.units, stride = gridDim.x * NWARP;
+    uint32_t unit = warp * gridDim.x + blockIdx.x;
+    uint64_t row_ahead = 0;
+    bool have_ahead = unit < n_units && token_row(p.ids, unit / p.units, row_ahead, lane == 0u && unit % p.units == 0u);
+    // the next group: the unit's next one, or the first of the next unit with a row
+    auto advance = [&](Item &it, bool in_unit) {
+        if (in_unit && it.g < it.last) {
+            ++it.g;
+        } else {
+            for (;;) {
+                if (unit >= n_units) return false;
+                const uint32_t t = unit / p.units, part = unit % p.units;
+                const bool have = have_ahead;
+                const uint64_t row = row_ahead;
+                unit += stride;
+                have_ahead = unit < n_units && token_row(p.ids, unit / p.units, row_ahead, lane == 0u && unit % p.units == 0u);
+                if (!have) {
+                    const uint32_t c0 = part * GROUP_SYMS;
+                    zero_row(p.out + t * p.ldo, c0, part + 1u < p.units ? c0 + GROUP_SYMS : p.dim, lane);
+                    continue;
+                }
+                it.t = t;
+                it.w0 = p.first + row * p.dim;
+                it.g = (uint32_t)(it.w0 / GROUP_SYMS) + part;
+                it.last = p.units > 1u ? it.g : (uint32_t)((it.w0 + p.dim - 1u) / GROUP_SYMS);
+                break;
+            }
+        }
+        it.s0 = __ldg(prm.group_start + it.g);
+        it.s1 = __ldg(prm.group_start + it.g + 1u);
+        return true;
+    };
+    // lane 0: chunk bits and stream span into slot s / the raw bytes
+    auto issue_stream = [&](const Item &it, uint32_t s) {
+        uint8_t *slot = wslots + s * slot_bytes;
+        const uint32_t bar = bar_s0 + 8u * s;
+        const uint64_t sb0 = (it.s0 >> 3) & ~15ull, d = it.s1 - it.s0;
+        uint32_t sbytes = 0;
+        if (sb0 < prm.stream_bytes) {  // (a corrupt plan copies a full slot and is rejected before it is decoded)
+            sbytes = min(span_bytes((uint32_t)it.s0 & 127u, d < (1u << 17) ? (uint32_t)d : (1u << 17)), prm.sbuf_bytes);
+            sbytes = (uint32_t)min((uint64_t)sbytes, prm.stream_bytes - sb0);
+        }
+        const bool cb_ok = check(it.g < prm.n_groups, CK_EMBED_COPY);
+        const bool st_ok = check(sbytes <= prm.sbuf_bytes && (sbytes == 0u || sb0 + sbytes <= prm.stream_bytes), CK_EMBED_COPY);
+        fence_proxy_async();
+        mbar_expect_tx(bar, (cb_ok ? 64u : 0u) + (st_ok ? sbytes : 0u));
+        if (cb_ok) bulk_load(smem_u32(slot), prm.chunk_bits + (size_t)it.g * GROUP_CHUNKS, 64u, bar);
+        if (st_ok && sbytes) bulk_load(smem_u32(slot + 64), prm.stream + sb0, sbytes, bar);
+    };
+    auto issue_mant = [&](const Item &it) {
+        const uint64_t m0 = (uint64_t)it.g * GROUP_SYMS;
+        const uint32_t bytes = (uint32_t)min((uint64_t)GROUP_SYMS, prm.mant_bytes - m0);
+        const bool ok = check(m0 < prm.mant_bytes && m0 + bytes <= prm.mant_bytes, CK_EMBED_COPY);
+        fence_proxy_async();
+        mbar_expect_tx(bar_m, ok ? bytes : 0u);
+        if (ok) bulk_load(smem_u32(mbuf), prm.mant + m0, bytes, bar_m);
+    };
+    Item cur = {}, nxt;
+    bool live = advance(cur, false);
+    if (live && lane == 0u) {
+        issue_stream(cur, 0);
+        issue_mant(cur);
+    }
+    nxt = cur;
+    bool more = live && advance(nxt, true);
+
+    __syncthreads();  // the table's barrier is initialised
+    const bool tok = mbar_wait(bar_t, 0u);
+    const bool bad = tok && check_fast_table<NT>(s_fast, n_fast, prm.fast_bits, (int)tid);
+    const bool all_in = __syncthreads_and(tok);
+    if (__syncthreads_or(bad || !all_in)) {  // a malformed table, or its copy never came: nothing is decoded
+        if (tid == 0u) {
+            atomicOr(&g_status, all_in ? ST_LUT : ST_TIMEOUT);
+            if (!all_in) mbar_wait_bounded(bar_t, 0u);
+        }
+        if (live && lane == 0u) {  // the copies in flight land first
+            mbar_wait(bar_s0, 0u);
+            mbar_wait(bar_m, 0u);
+        }
+        return;
+    }
+
+    for (uint32_t k = 0; live; ++k) {
+        const uint32_t s = k & 1u;
+        const uint8_t *slot = wslots + s * slot_bytes;
+        __syncwarp();  // every lane is done with the other slot
+        if (more && lane == 0u) issue_stream(nxt, s ^ 1u);
+
+        bool ok = mbar_wait(bar_s0 + 8u * s, (k >> 1) & 1u);
+        const uint32_t cbits = reinterpret_cast<const uint16_t *>(slot)[lane];
+        uint32_t incl = cbits;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+            if (lane >= (uint32_t)d) incl += y;
+        }
+        const uint32_t excl = incl - cbits, gbits = __shfl_sync(0xFFFFFFFFu, incl, 31);
+        const uint32_t c = cur.g * GROUP_CHUNKS + lane, n = chunk_weights(prm, c);
+        const uint32_t r0 = (uint32_t)cur.s0 & 127u, span = span_bytes(r0, gbits);
+        const bool valid = __all_sync(0xFFFFFFFFu, cur.s1 - cur.s0 == gbits && cbits <= 32u * LANE_SYMS && span <= prm.sbuf_bytes &&
+                                                       ((cur.s0 >> 3) & ~15ull) + span <= prm.stream_bytes &&
+                                                       (n != 0u || cbits == 0u));
+        const uint64_t cw = (uint64_t)c * LANE_SYMS, end = cur.w0 + p.dim;
+        uint32_t err = 0;
+        if (ok && valid && cw < end && cw + n > cur.w0) {  // the row touches this chunk
+            const uint32_t r = r0 + excl;
+            uint32_t rd_end, wr_end;
+            const uint32_t to = decode_chunk(smem_u32(slot + 64), r, (int)(8u * n), smem_u32(s_fast), kshift, g_hier,
+                                             prm.n_tables, exps, err, rd_end, wr_end);
+            if (to != r + cbits) err |= ST_COUNT;
+            check(rd_end <= smem_u32(wbase) + wbytes, CK_EMBED_READ);
+            check(wr_end < exps + EXP_STRIDE * EXP_WORDS, CK_EMBED_READ);
+        }
+        Item ahead = nxt;
+        const bool ahead_live = more && advance(ahead, true);
+        ok = mbar_wait(bar_m, k & 1u) && ok;
+        if (!__all_sync(0xFFFFFFFFu, ok)) {  // a bulk copy never completed: give up
+            if (lane == 0u) {  // report, then give each copy in flight one more bounded wait
+                atomicOr(&g_status, ST_TIMEOUT);
+                mbar_wait_bounded(bar_s0 + 8u * s, (k >> 1) & 1u);
+                mbar_wait_bounded(bar_m, k & 1u);
+                if (more) mbar_wait_bounded(bar_s0 + 8u * (s ^ 1u), ((k + 1u) >> 1) & 1u);
+            }
+            return;
+        }
+        const bool good = valid && !__any_sync(0xFFFFFFFFu, err != 0u);
+        if (!valid) {
+            if (lane == 0u) atomicOr(&g_status, ST_RANGE);
+        } else if (!good) {
+            if (err) atomicOr(&g_status, err);
+        } else {
+            __syncwarp();  // the join reads other lanes' exponent slots
+            const uint64_t g0 = (uint64_t)cur.g * GROUP_SYMS;
+            uint16_t *out = p.out + cur.t * p.ldo;
+            if constexpr (V == 16) {
+                const uint32_t mrow = smem_u32(mbuf) + 16u * lane, erow = exps0 + 4u * (lane >> 2) + 4u * EXP_STRIDE * (lane & 3u);
+#pragma unroll
+                for (uint32_t j = 0; j < 4u; ++j) {
+                    const uint64_t w = g0 + 512u * j + 16u * lane;
+                    if (w < cur.w0 || w >= end) continue;
+                    uint4 a, b;
+                    join16(mrow + 512u * j, erow + 32u * j, a, b);
+                    stg256_cs(out + (w - cur.w0), scaled8(a, p.scale, one), scaled8(b, p.scale, one));
+                }
+            } else if constexpr (V == 8) {
+#pragma unroll
+                for (uint32_t j = 0; j < 8u; ++j) {  // piece lane + 32 j: words 2 (piece mod 8) and + 1 of chunk piece / 8
+                    const uint32_t piece = lane + 32u * j;
+                    const uint64_t w = g0 + 8u * piece;
+                    if (w < cur.w0 || w >= end) continue;
+                    const uint32_t e = exps0 + 4u * (piece >> 3) + 2u * EXP_STRIDE * (piece & 7u), m = smem_u32(mbuf) + 8u * piece;
+                    uint4 v;
+                    join4(lds32(e), lds32(m), v.x, v.y);
+                    join4(lds32(e + EXP_STRIDE), lds32(m + 4u), v.z, v.w);
+                    __stcs(reinterpret_cast<uint4 *>(out + (w - cur.w0)), scaled8(v, p.scale, one));
+                }
+            } else {
+                const uint32_t lo = (uint32_t)(max(cur.w0, g0) - g0), hi = (uint32_t)(min(end, g0 + GROUP_SYMS) - g0);
+#pragma unroll 4
+                for (uint32_t i = lo + lane; i < hi; i += 32u) {
+                    const uint32_t word = lds32(exps0 + 4u * (i >> 6) + EXP_STRIDE * ((i & 63u) >> 2));
+                    out[g0 + i - cur.w0] = scaled1(join1((word >> (8u * (i & 3u))) & 0xFFu, mbuf[i]), p.scale, one);
+                }
+            }
+        }
+        if (!more) break;
+        __syncwarp();  // every lane has read the raw bytes
+        if (lane == 0u) issue_mant(nxt);
+        cur = nxt;
+        nxt = ahead;
+        more = ahead_live;
+    }
+}
+
+// Rows of a scope with one exponent (no stream): raw bytes joined with it.
+template <int V>
+__global__ void __launch_bounds__(256) embed_single_rows(const RowsOfLanes p) {
+    const bool one = p.scale == 1.f;
+    const uint32_t E = rot_sym(p.single) * 0x01010101u, lane = threadIdx.x & 31u;
+    for (uint32_t t = blockIdx.x * 8u + (threadIdx.x >> 5); t < p.ids.tokens; t += gridDim.x * 8u) {
         uint64_t row = 0;
-        const bool have = token_row(p.ids, t, row, lane == 0u);
         uint16_t *out = p.out + t * p.ldo;
-        if (!have) {
-            if (item % p.row_groups == 0u)
-                for (uint32_t c = lane; c < p.dim; c += 32u) out[c] = 0;
+        if (!token_row(p.ids, t, row, lane == 0u)) {
+            zero_row(out, 0u, p.dim, lane);
             continue;
         }
-        const uint64_t w0 = p.first + row * p.dim, w1 = w0 + p.dim;
-        const uint64_t g = w0 / GROUP_SYMS + item % p.row_groups;
-        if (g * GROUP_SYMS >= w1) continue;
-        const uint64_t c = g * GROUP_CHUNKS + lane;  // this lane's chunk
-        const bool need = c * LANE_SYMS < w1 && (c + 1u) * LANE_SYMS > w0;
-        bool ok = true;
-        uint32_t err = 0;
-        __syncwarp();  // the previous item's slots have been read
-        if (p.total_bits == 0u) {
-            for (uint32_t k = 0; k < 16u; ++k) s_exp[warp][32u * k + lane] = rot_sym(p.single) * 0x01010101u;
-        } else {
-            const uint64_t gs0 = __ldg(p.lanes.group_start + g), gs1 = __ldg(p.lanes.group_start + g + 1);
-            const uint32_t cbits = __ldg(p.lanes.chunk_bits + c);
-            uint32_t incl = cbits;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, incl, d);
-                if (lane >= (uint32_t)d) incl += y;
+        const uint8_t *m = p.lanes.mant + p.first + row * p.dim;
+#pragma unroll 4
+        for (uint32_t c = V * lane; c < p.dim; c += 32u * V) {
+            if constexpr (V == 8) {
+                const uint2 b = __ldg(reinterpret_cast<const uint2 *>(m + c));
+                uint4 v;
+                join4(E, b.x, v.x, v.y);
+                join4(E, b.y, v.z, v.w);
+                __stcs(reinterpret_cast<uint4 *>(out + c), scaled8(v, p.scale, one));
+            } else {
+                out[c] = scaled1(join1(E & 0xFFu, __ldg(m + c)), p.scale, one);
             }
-            const uint32_t gbits = __shfl_sync(0xFFFFFFFFu, incl, 31);
-            ok = __all_sync(0xFFFFFFFFu, cbits <= 32u * LANE_SYMS) && gs1 - gs0 == gbits && gs1 <= p.total_bits;
-            if (ok && need) {
-                const uint32_t n = chunk_weights(p.lanes, (uint32_t)c);
-                const uint64_t start = gs0 + incl - cbits;
-                const uint32_t *words = reinterpret_cast<const uint32_t *>(p.lanes.stream);
-                const uint64_t last = p.lanes.stream_bytes / 4u - 1u;
-                uint64_t at = start >> 5;
-                uint32_t a = bswap32(__ldg(words + min(at, last))), b = bswap32(__ldg(words + min(at + 1u, last)));
-                uint32_t nxt = __ldg(words + min(at + 2u, last));
-                uint32_t pos = (uint32_t)start & 31u, used = 0, acc = 0;
-                for (uint32_t i = 0; i < n; ++i) {
-                    const uint32_t x = __funnelshift_l(b, a, pos);
-                    uint32_t e = s_root[x >> 24];
-                    if (e & LUT_PTR) e = resolve_escape(x, hier, p.lanes.n_tables);
-                    if (e & ESC_BAD) err |= ST_LUT;
-                    const uint32_t len = (e >> LUT_LEN_SHIFT) & 63u;
-                    used += len;
-                    pos += len;
-                    if (pos >= 32u) {
-                        pos -= 32u;
-                        a = b;
-                        b = bswap32(nxt);
-                        ++at;
-                        nxt = __ldg(words + min(at + 2u, last));
-                    }
-                    acc |= rot_sym(e) << (8u * (i & 3u));
-                    if ((i & 3u) == 3u || i + 1u == n) {
-                        s_exp[warp][32u * (i >> 2) + lane] = acc;
-                        acc = 0;
-                    }
-                }
-                if (used != cbits) err |= ST_COUNT;
-            }
-        }
-        if (!__all_sync(0xFFFFFFFFu, ok && err == 0u)) {
-            if (!ok) err = ST_RANGE;
-            if (err) atomicOr(&g_status, err);
-            continue;  // a damaged group writes nothing
-        }
-        __syncwarp();  // the join reads other lanes' slots
-        const uint64_t lo = max(w0, g * GROUP_SYMS), hi = min(w1, (g + 1u) * GROUP_SYMS);
-        for (uint64_t w = lo + lane; w < hi; w += 32u) {
-            const uint32_t i = (uint32_t)(w % LANE_SYMS), ch = (uint32_t)(w / LANE_SYMS % GROUP_CHUNKS);
-            const uint32_t e = (s_exp[warp][32u * (i >> 2) + ch] >> (8u * (i & 3u))) & 0xFFu;
-            out[w - w0] = scaled(join1(e, __ldg(p.lanes.mant + w)), p.scale, one);
         }
     }
 }
@@ -643,9 +838,39 @@ dfw_status launch_embed_rows(const uint16_t *d_table, uint64_t rows, uint32_t di
     p.ldo = ld_out;
     p.dim = dim;
     p.scale = scale;
-    const uint64_t want = (tokens + 7u) / 8u, cap = (uint64_t)sms * 8u;
-    embed_table_rows<<<(unsigned)(want < cap ? want : cap), 256, 0, s>>>(p);
-    return cudaGetLastError() == cudaSuccess ? DFW_OK : DFW_ECUDA;
+    const bool vec = dim % 8u == 0u && ((reinterpret_cast<uintptr_t>(d_table) | reinterpret_cast<uintptr_t>(d_out)) & 15u) == 0u &&
+                     (rows == 1u || ld_table % 8u == 0u) && (tokens == 1u || ld_out % 8u == 0u);
+    p.parts = (dim + EMBED_PART - 1u) / EMBED_PART;
+    return launch_with(vec ? embed_table_rows<8> : embed_table_rows<1>, (tokens * p.parts + 7u) / 8u, 256, 0, false, 1, s, p);
+}
+
+// One CTA shape and join width of embed_lanes_rows.
+template <int NT, int V>
+dfw_status launch_embed_groups(const RowsOfLanes &p, uint32_t smem, int sms, cudaStream_t s) {
+    static int opted[16];
+    int dev = 0, per_sm = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 16) return DFW_ECUDA;
+    const auto fn = embed_lanes_rows<NT, V>;
+    if (!opted[dev]) {
+        if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MOST) != cudaSuccess) return DFW_ECUDA;
+        opted[dev] = 1;
+    }
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, NT, smem) != cudaSuccess) return DFW_ECUDA;
+    if (per_sm < 1) return DFW_EINVAL;
+    const uint64_t ctas = ((uint64_t)p.ids.tokens * p.units + NT / 32 - 1u) / (NT / 32);
+    return launch_with(fn, std::min<uint64_t>(ctas, (uint64_t)per_sm * sms), NT, smem, false, 1, s, p);
+}
+
+template <int V>
+dfw_status launch_embed_width(const RowsOfLanes &p, int sms, cudaStream_t s) {
+    const uint32_t table = 8u << p.lanes.fast_bits, warp = warp_smem_bytes(p.lanes.sbuf_bytes);
+    // the largest CTA that fits shares one copy of the table among most warps;
+    // up to four groups per SM go to small ones, a group per warp
+    const uint64_t units = (uint64_t)p.ids.tokens * p.units;
+    if (units > 4u * (uint64_t)sms && table + 32u * warp <= SMEM_MOST) return launch_embed_groups<1024, V>(p, table + 32u * warp, sms, s);
+    if (units > 4u * (uint64_t)sms && table + 16u * warp <= SMEM_MOST) return launch_embed_groups<512, V>(p, table + 16u * warp, sms, s);
+    if (table + 4u * warp > SMEM_MOST) return launch_embed_groups<32, V>(p, table + warp, sms, s);
+    return launch_embed_groups<128, V>(p, table + 4u * warp, sms, s);
 }
 
 dfw_status launch_embed_lanes(const dfw_lanes_scope *scope, uint64_t first, uint64_t rows, uint32_t dim,
@@ -680,14 +905,20 @@ dfw_status launch_embed_lanes(const dfw_lanes_scope *scope, uint64_t first, uint
     p.dim = dim;
     p.single = table->single_symbol;
     p.scale = scale;
-    // whole groups per row when every row starts on a group boundary or rows
-    // divide a group; else a row may touch one group more
-    const uint32_t whole = (dim + GROUP_SYMS - 1u) / GROUP_SYMS;
-    const bool even = first % GROUP_SYMS == 0u && (dim % GROUP_SYMS == 0u || GROUP_SYMS % dim == 0u);
-    p.row_groups = even ? whole : (dim + GROUP_SYMS - 2u) / GROUP_SYMS + 1u;
-    const uint64_t want = (tokens * p.row_groups + 3u) / 4u, cap = (uint64_t)sms * 16u;
-    embed_lanes_rows<<<(unsigned)(want < cap ? want : cap), 128, 0, s>>>(p);
-    return cudaGetLastError() == cudaSuccess ? DFW_OK : DFW_ECUDA;
+    const bool out16 = (reinterpret_cast<uintptr_t>(d_out) & 15u) == 0u && (tokens == 1u || ld_out % 8u == 0u);
+    const bool out32 = (reinterpret_cast<uintptr_t>(d_out) & 31u) == 0u && (tokens == 1u || ld_out % 16u == 0u);
+    if (table->total_bits == 0u) {
+        const uint64_t want = (tokens + 7u) / 8u;
+        const bool vec = out16 && first % 8u == 0u && dim % 8u == 0u;
+        return launch_with(vec ? embed_single_rows<8> : embed_single_rows<1>, std::min<uint64_t>(want, (uint64_t)sms * 8u), 256, 0,
+                           false, 1, s, p);
+    }
+    const bool whole = first % GROUP_SYMS == 0u && (dim % GROUP_SYMS == 0u || GROUP_SYMS % dim == 0u);
+    p.units = whole ? (dim + GROUP_SYMS - 1u) / GROUP_SYMS : 1u;
+    if (tokens * p.units > 0x7FFFFFFFull) return DFW_EINVAL;
+    if (out32 && first % 16u == 0u && dim % 16u == 0u) return launch_embed_width<16>(p, sms, s);
+    if (out16 && first % 8u == 0u && dim % 8u == 0u) return launch_embed_width<8>(p, sms, s);
+    return launch_embed_width<1>(p, sms, s);
 }
 
 // How the gradient of `tokens` tokens is cut: blocks of `block` tokens that a

@@ -72,6 +72,8 @@ enum CheckSite : uint32_t {
     CK_ENC_PACK_BUF = 15,       // encoder packing beyond its shared word buffer
     CK_ENC_PACK_STREAM = 16,    // encoder packing beyond the stream
     CK_CLOSED_READ = 17,        // a closed-form decode read past the stream
+    CK_EMBED_COPY = 18,         // an embedding row's group copied beyond its buffers or slot
+    CK_EMBED_READ = 19,         // an embedding row's stream reads or exponent slots past their areas
 };
 
 // A named range on profiler timelines (NVTX) for the duration of a call;

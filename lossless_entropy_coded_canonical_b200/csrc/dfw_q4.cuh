@@ -82,6 +82,8 @@ dfw_status launch_with(F fn, uint64_t grid, unsigned block, uint32_t smem, bool 
     return cudaLaunchKernelEx(&cfg, fn, args...) == cudaSuccess ? DFW_OK : DFW_ECUDA;
 }
 
+constexpr uint32_t SMEM_MOST = 227u * 1024u;  // a CTA's largest shared memory
+
 // ----------------------------------------------------------------- 4-bit tiles
 
 constexpr uint32_t Q4_ROWS = 16, Q4_COLS = 128, Q4_CODES = 1024;
@@ -623,8 +625,6 @@ q4_fn q4_variant(const Q4Params &q, int nt, uint32_t warps, bool split) {
         default: return q.zeros ? q4_variant<4, true>(nt, warps, split) : q4_variant<4, false>(nt, warps, split);
     }
 }
-
-constexpr uint32_t SMEM_MOST = 227u * 1024u;
 
 dfw_status launch_q4_pass(Q4GemvParams a, int dev, int sms, cudaStream_t s) {
     const int nt = a.m > 8u ? 2 : 1;
