@@ -643,25 +643,25 @@ def q4_gemv(q: Q4Weights, x: torch.Tensor, out: torch.Tensor | None = None, out_
     [tokens, cols] or [cols], at most 64 tokens; returns fp32 or bf16
     [tokens, rows] or [rows].  Several matrices with the same input (q, k, v;
     gate, up) are best held as one, their rows one below the other."""
-    dev = q.packed.device
-    rows, cols = q.shape
-    _expect("x", x, dev, _BF16, x.dim() if x.dim() in (1, 2) else 2)
-    if x.shape[-1] != cols:
-        raise ValueError(f"x has {x.shape[-1]} columns, the matrix {cols}")
-    x2 = x if x.dim() == 2 else x[None]
-    m = x2.shape[0]
+    info, dev, shape = q.info, q.packed.device, x.shape
+    rows, cols, nd = info.rows, info.cols, len(shape)
+    if nd not in (1, 2) or shape[-1] != cols:
+        raise ValueError(f"x must be [tokens, {cols}] or [{cols}], not {list(shape)}")
+    _expect("x", x, dev, _BF16, nd)
+    m = shape[0] if nd == 2 else 1
+    want = (m, rows) if nd == 2 else (rows,)
     with _On(dev, stream) as sh:
         if out is None:
             if out_dtype not in _FLOATS:
                 raise TypeError(f"out_dtype {out_dtype}, expected one of {_FLOATS}")
-            out = torch.empty((*x.shape[:-1], rows), dtype=out_dtype, device=dev)
+            out = torch.empty(want, dtype=out_dtype, device=dev)
         else:
-            _expect("out", out, dev, _FLOATS, x.dim())
-            if out.shape != (*x.shape[:-1], rows):
-                raise ValueError(f"out must have shape {(*x.shape[:-1], rows)}")
-        _check(lib().dfw_q4_gemv(q.packed.data_ptr(), ctypes.byref(q.info), m, x2.data_ptr(), _ld(x2, cols),
-                                 out.data_ptr(), int(out.dtype == torch.float32),
-                                 out.stride(0) if x.dim() == 2 and m > 1 else rows, sh), "dfw_q4_gemv")
+            _expect("out", out, dev, _FLOATS, nd)
+            if out.shape != want:
+                raise ValueError(f"out must have shape {want}")
+        _check(lib().dfw_q4_gemv(q.packed.data_ptr(), ctypes.byref(info), m, x.data_ptr(),
+                                 x.stride(0) if m > 1 else cols, out.data_ptr(), int(out.dtype == torch.float32),
+                                 out.stride(0) if m > 1 else rows, sh), "dfw_q4_gemv")
     return out
 
 
