@@ -376,8 +376,8 @@ __global__ void __launch_bounds__(256) embed_single_rows(const RowsOfLanes p) {
 // ------------------------------------------------------ the table's gradient
 
 // Sorting.  A cluster of C CTAs sorts a block of up to 1024 C IPT tokens by
-// row, stably: 8 bits a pass from the lowest.  Each warp ranks its own run of
-// tokens (equal digits of 32 tokens found by eight ballots: no atomics, a
+// row, stably: up to 8 bits a pass from the lowest.  Each warp ranks its own run of
+// tokens (equal digits of 32 tokens found by a ballot per bit: no atomics, a
 // fixed order); each CTA puts its tokens in digit order in its own shared
 // memory, and from there, with the other CTAs' digit counts read through
 // distributed shared memory, in their places in the cluster's order: the
@@ -390,7 +390,7 @@ struct SortParams {
     IdSource ids;
     uint32_t *keys, *pos;  // per block: sorted keys and the tokens they belong to
     uint32_t *joins;       // the two counters of JoinLists, cleared here
-    uint32_t passes;
+    uint32_t passes, bits;  // digits of a key and their width, at most 8
 };
 
 template <int C, int IPT>
@@ -421,16 +421,17 @@ __global__ void __launch_bounds__(SORT_THREADS, 1) grad_sort(const SortParams p)
         if (pos[j] < p.ids.tokens) key[j] = token_row(p.ids, pos[j], row, true) ? (uint32_t)row : (uint32_t)p.ids.rows;
     }
     for (uint32_t pass = 0; pass < p.passes; ++pass) {
-        const uint32_t shift = 8u * pass;
+        const uint32_t shift = p.bits * pass, mask = (1u << p.bits) - 1u;
         for (uint32_t i = lane; i < 256u; i += 32u) cnt[warp * SORT_STRIDE + i] = 0u;
         __syncwarp();
         uint32_t at[IPT];
 #pragma unroll
         for (int j = 0; j < IPT; ++j) {
-            const uint32_t d = (key[j] >> shift) & 255u;
+            const uint32_t d = (key[j] >> shift) & mask;
             uint32_t same = 0xFFFFFFFFu;
 #pragma unroll
-            for (int b = 0; b < 8; ++b) {
+            for (uint32_t b = 0; b < 8u; ++b) {
+                if (b >= p.bits) break;
                 const uint32_t v = __ballot_sync(0xFFFFFFFFu, (d >> b) & 1u);
                 same &= (d >> b) & 1u ? v : ~v;
             }
@@ -483,7 +484,7 @@ __global__ void __launch_bounds__(SORT_THREADS, 1) grad_sort(const SortParams p)
         __syncthreads();
 #pragma unroll
         for (int j = 0; j < IPT; ++j) {
-            const uint32_t to = cnt[warp * SORT_STRIDE + ((key[j] >> shift) & 255u)] + at[j];
+            const uint32_t to = cnt[warp * SORT_STRIDE + ((key[j] >> shift) & mask)] + at[j];
             l_key[to] = key[j];
             l_pos[to] = pos[j];
         }
@@ -504,7 +505,7 @@ __global__ void __launch_bounds__(SORT_THREADS, 1) grad_sort(const SortParams p)
 #pragma unroll
             for (int j = 0; j < IPT; ++j) {
                 const uint32_t from = run + 32u * j, k = l_key[from];
-                const uint32_t to = from + shift_by[(k >> shift) & 255u], r = to / CAP, i = to % CAP;
+                const uint32_t to = from + shift_by[(k >> shift) & mask], r = to / CAP, i = to % CAP;
                 st_cluster(map_rank(smem_u32(s_key + i), r), k);
                 st_cluster(map_rank(smem_u32(s_pos + i), r), l_pos[from]);
             }
@@ -804,9 +805,15 @@ __global__ void __launch_bounds__(256) grad_join(const ReduceParams p) {
         const uint32_t key = __ldg(p.keys + (uint64_t)(w + 1u) * p.window);
         float sum[VEC] = {};
         add(sum, w, 1u, col);
+        Pack<float, VEC> v[JOIN_FEW - 1];  // (all loads first; those past the row's windows read its last one again)
 #pragma unroll
         for (uint32_t k = 1; k < JOIN_FEW; ++k)
-            if (k <= more) add(sum, w + k, 0u, col);
+            v[k - 1u] = *reinterpret_cast<const Pack<float, VEC> *>(p.partial + (uint64_t)(w + min(k, more)) * 2u * p.dim + col);
+#pragma unroll
+        for (uint32_t k = 1; k < JOIN_FEW; ++k) {
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) sum[j] += k <= more ? v[k - 1u].v[j] : 0.f;
+        }
         put_row<OUT, VEC>(p.grad, (uint64_t)key * p.dim + col, sum, p.scale, p.accumulate != 0u);
     }
 }
@@ -1017,13 +1024,22 @@ struct GradCut {
     uint64_t list;   // bytes of one array of keys or positions
 };
 
-GradCut grad_cut(uint64_t tokens) {
+GradCut grad_cut(uint64_t tokens, uint32_t dim) {
     GradCut c;
     c.ctas = tokens <= 1024u ? 1u : 8u;
     c.ipt = tokens <= 8192u ? 1u : tokens <= 32768u ? 4u : 8u;
     c.block = SORT_THREADS * c.ctas * c.ipt;
     c.blocks = (uint32_t)((tokens + c.block - 1u) / c.block);
-    c.window = tokens <= 1024u ? 8u : tokens <= (1u << 14) ? 32u : tokens <= (1u << 17) ? 64u : 128u;
+    // Windows such that the summing CTAs (128 threads of 8 columns, 6 to an SM
+    // of 148) all run at once where windows of 16 (64 for many tokens) to 128
+    // allow it: a second, almost empty round of CTAs would double the time.
+    // (65536 x 1024: 65.1 us with windows of 80, 72.8 with 64; 60000 x 64: 44.4
+    // with 64, 49.1 with 16, whose partial sums outweigh the shorter walks.)
+    uint64_t threads = 8u;
+    while (threads < 128u && threads * 8u < dim) threads *= 2u;
+    threads *= (dim + 8u * threads - 1u) / (8u * threads);
+    const uint64_t window = (tokens * threads + 128u * 888u - 1u) / (128u * 888u);
+    c.window = (uint32_t)std::min<uint64_t>(128u, std::max<uint64_t>(tokens <= 1024u ? 8u : tokens <= 16384u ? 16u : 64u, (window + 7u) & ~7ull));
     c.windows = (uint32_t)((tokens + c.window - 1u) / c.window);
     c.list = (tokens * 4u + 15u) & ~15ull;
     c.joins = ((4u + 2u * c.windows) * 4u + 15u) & ~15u;
@@ -1032,7 +1048,7 @@ GradCut grad_cut(uint64_t tokens) {
 
 uint64_t embed_grad_scratch(uint64_t tokens, uint32_t dim) {
     if (tokens == 0u) return 0u;
-    const GradCut c = grad_cut(tokens);
+    const GradCut c = grad_cut(tokens, dim);
     return c.joins + c.list * (c.blocks > 1u ? 4u : 2u) + (c.windows > 1u ? (uint64_t)c.windows * 2u * dim * 4u : 0u);
 }
 
@@ -1107,15 +1123,17 @@ dfw_status launch_embed_grad(const void *d_ids, int ids64, uint64_t tokens, cons
     const uint64_t fill_bytes = accumulate ? 0u : rows * dim * (grad_fp32 ? 4u : 2u);
     const uint64_t fillers = std::min<uint64_t>((fill_bytes + (1u << 14) - 1u) >> 14, (uint64_t)sms * 4u);
     if (tokens == 0u) return launch_with(grad_zero, fillers, 512, 0, false, 1, s, fill, fill_bytes);
-    const GradCut cut = grad_cut(tokens);
+    const GradCut cut = grad_cut(tokens, dim);
     uint8_t *const scratch = static_cast<uint8_t *>(d_scratch);
     uint32_t *lists[4];
     for (int i = 0; i < 4; ++i) lists[i] = reinterpret_cast<uint32_t *>(scratch + cut.joins + i * cut.list);
     sp.keys = lists[0];
     sp.pos = lists[1];
     sp.joins = reinterpret_cast<uint32_t *>(scratch);
-    sp.passes = 1u;
-    while (rows >> (8u * sp.passes)) ++sp.passes;  // keys go up to `rows`
+    uint32_t key_bits = 1u;
+    while (rows >> key_bits) ++key_bits;  // keys go up to `rows`
+    sp.passes = (key_bits + 7u) / 8u;
+    sp.bits = (key_bits + sp.passes - 1u) / sp.passes;
     st = cut.ctas == 1u ? launch_grad_sort<1, 1>(sp, cut.blocks, s)
          : cut.ipt == 1u ? launch_grad_sort<8, 1>(sp, cut.blocks, s)
          : cut.ipt == 4u ? launch_grad_sort<8, 4>(sp, cut.blocks, s)
