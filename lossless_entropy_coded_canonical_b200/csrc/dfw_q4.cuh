@@ -315,17 +315,19 @@ __device__ __forceinline__ void q4_expand(uint32_t word, uint32_t off, uint32_t 
     e[3] = fma_bf16x2(up & 0x00F000F0u, HIGH, off);
 }
 
-// A tile as one lane takes it from the ring (shared address `tile`): its words
-// of both row halves, and the scales and zero points of rows g and g + 8.
+// A tile as one lane takes it from the ring: its words of both row halves
+// (from shared address cp, the tile + 16 lane), and the scales and zero points
+// of rows g and g + 8 (from sp, the tile + 2 GT g).
 template <int GT, bool Z>
 struct Q4Tile {
     uint4 lo, hi;
     uint32_t s[GT == 4 ? 4 : 2];  // GT = 4: two words per row, else one
     uint32_t z[Z ? 2 : 1];
-    __device__ __forceinline__ Q4Tile(uint32_t tile, uint32_t lane) {
-        const uint32_t g = lane >> 2, sp = tile + Q4_CODES + 2u * GT * g, zp = tile + Q4_CODES + 32u * GT + GT * g;
-        lo = lds128(tile + 16u * lane);
-        hi = lds128(tile + 512u + 16u * lane);
+    __device__ __forceinline__ Q4Tile(uint32_t cp, uint32_t sp, uint32_t g) {
+        const uint32_t zp = sp + Q4_CODES + 32u * GT - GT * g;
+        lo = lds128(cp);
+        hi = lds128(cp + 512u);
+        sp += Q4_CODES;
         if constexpr (GT == 4) {
             s[0] = lds32(sp), s[1] = lds32(sp + 4u), s[2] = lds32(sp + 64u), s[3] = lds32(sp + 68u);
         } else if constexpr (GT == 2) {
@@ -399,7 +401,7 @@ __global__ void __launch_bounds__(32 * W, 1) q4_gemv_tiles(const Q4GemvParams a)
     const uint32_t split = SPLIT ? a.split : 1u, rank = blockIdx.x % split, me = blockIdx.x / split;
     const uint32_t ct0 = rank * a.tiles, cts = ct0 < a.q.col_tiles ? min(a.tiles, a.q.col_tiles - ct0) : 0u;
     const uint32_t rt0 = me * a.share + min(me, a.extra), rows = a.share + (me < a.extra ? 1u : 0u);  // row tiles
-    const uint32_t ring = smem_u32(smem) + warp * RING * SLOT;
+    const uint32_t ring = smem_u32(smem) + warp * RING * SLOT + 16u * lane;  // a lane's own place in it
     float *sums = reinterpret_cast<float *>(smem + W * RING * SLOT);
     uint8_t *vecs = reinterpret_cast<uint8_t *>(sums + (W + a.pass - 1u) * outs);
     float *join = reinterpret_cast<float *>(vecs + a.m * a.pitch);
@@ -422,19 +424,30 @@ __global__ void __launch_bounds__(32 * W, 1) q4_gemv_tiles(const Q4GemvParams a)
             src = a.packed + ((uint64_t)(rt0 + in_row + lo / cts) * a.q.col_tiles + ct0 + in_ct) * TILE + 16u * lane;
             in_row += n;
         }
+        if (in_left >= Q4_STEP && (!SPLIT || in_ct + Q4_STEP <= cts)) {  // a whole step, contiguous
 #pragma unroll
-        for (uint32_t u = 0; u < Q4_STEP; ++u) {
-            if (in_left == 0u) break;
-            const uint32_t dst = slot_in + u * TILE + 16u * lane;
-            cp_async16(dst, src);
-            cp_async16(dst + 512u, src + 512);
-            if (lane < (TILE - Q4_CODES) / 16u) cp_async16(dst + Q4_CODES, src + Q4_CODES);
-            src += TILE;
-            if (SPLIT && ++in_ct == cts) {
+            for (uint32_t at = 0; at < SLOT; at += 512u)
+                if (at + 512u <= SLOT || lane < (SLOT - at) / 16u) cp_async16(slot_in + at, src + at);
+            src += SLOT;
+            in_left -= Q4_STEP;
+            in_ct += Q4_STEP;
+            if (SPLIT && in_ct == cts) {
                 in_ct = 0;
                 src += (uint64_t)(a.q.col_tiles - cts) * TILE;
             }
-            --in_left;
+        } else {
+            for (uint32_t u = 0; u < Q4_STEP && in_left; ++u) {
+                const uint32_t dst = slot_in + u * TILE;
+                cp_async16(dst, src);
+                cp_async16(dst + 512u, src + 512);
+                if (lane < (TILE - Q4_CODES) / 16u) cp_async16(dst + Q4_CODES, src + Q4_CODES);
+                src += TILE;
+                if (SPLIT && ++in_ct == cts) {
+                    in_ct = 0;
+                    src += (uint64_t)(a.q.col_tiles - cts) * TILE;
+                }
+                --in_left;
+            }
         }
         slot_in = next_slot(slot_in);
         cp_async_commit();
@@ -493,7 +506,7 @@ __global__ void __launch_bounds__(32 * W, 1) q4_gemv_tiles(const Q4GemvParams a)
 #pragma unroll
             for (uint32_t u = 0; u < Q4_STEP; ++u) {
                 if (i + u >= hi) break;
-                q4_tile_products<GT, Z, NT>(Q4Tile<GT, Z>(slot + u * TILE, lane), x0 + 256u * ct, nt_step, acc);
+                q4_tile_products<GT, Z, NT>(Q4Tile<GT, Z>(slot + u * TILE, slot + u * TILE - 16u * lane + 2u * GT * g, g), x0 + 256u * ct, nt_step, acc);
                 if (++ct == cts) {
                     put_away(row++);
                     ct = 0;
