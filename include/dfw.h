@@ -782,8 +782,9 @@ dfw_status dfw_embed_rows(const uint16_t *d_table, uint64_t rows, uint32_t dim, 
  *               token points).  accumulate 1: rows that tokens point to are
  *               added to, one rounding per element and call; others are not touched
  *   d_scratch   device, 16-byte aligned, scratch_bytes >=
- *               dfw_embed_grad_scratch_bytes(tokens, dim); calls that overlap
- *               in time need one each
+ *               dfw_embed_grad_scratch_bytes(tokens, dim) (0 for few tokens:
+ *               then d_scratch may be NULL); calls that overlap in time need
+ *               one each
  * d_grad must not overlap an input.  Limits as above.  Asynchronous.
  * Errors: DFW_EINVAL, DFW_EALIGN, DFW_ENOMEM (scratch too small), DFW_ECUDA.
  */

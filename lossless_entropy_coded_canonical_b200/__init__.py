@@ -551,17 +551,12 @@ class _On:
 
 
 def _expect(name: str, t: torch.Tensor, device: torch.device, dtypes, dim: int | None = None) -> None:
-    if not t.is_cuda or t.device != device:
+    if t.device != device or device.type != "cuda":
         raise ValueError(f"{name} must be on {device if device.type == 'cuda' else 'a CUDA device'}, not {t.device}")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
     if dim is not None and (t.dim() != dim or (t.numel() and t.stride(-1) != 1)):
         raise ValueError(f"{name} must have {dim} dimensions, the last one contiguous")
-
-
-def _ld(t: torch.Tensor, width: int) -> int:
-    """Elements from one row to the next (a single row's is not used)."""
-    return t.stride(0) if t.shape[0] > 1 else width
 
 
 _BF16, _F32 = (torch.bfloat16,), (torch.float32,)
@@ -624,7 +619,7 @@ def q4_quantise(w: torch.Tensor, group: int = 128, zeros: bool = False, stream=N
     _expect("w", w, w.device, _BF16, 2)
     with _On(w.device, stream) as sh:
         q = _q4_new(w.shape[0], w.shape[1], group, zeros, w.device)
-        _check(lib().dfw_q4_quantise(w.data_ptr(), _ld(w, w.shape[1]), ctypes.byref(q.info), q.packed.data_ptr(), sh),
+        _check(lib().dfw_q4_quantise(w.data_ptr(), w.stride(0) if w.shape[0] > 1 else w.shape[1], ctypes.byref(q.info), q.packed.data_ptr(), sh),
                "dfw_q4_quantise")
     return q
 
@@ -669,16 +664,22 @@ def _embed_out(ids: torch.Tensor, dim: int, out, dev) -> torch.Tensor:
     _expect("ids", ids, dev, _IDS)
     if not ids.is_contiguous():
         raise ValueError("ids must be contiguous")
+    shape = (*ids.shape, dim)
     if out is None:
-        return torch.empty((*ids.shape, dim), dtype=torch.bfloat16, device=dev)
+        return torch.empty(shape, dtype=torch.bfloat16, device=dev)
     _expect("out", out, dev, _BF16)
-    if out.shape != (*ids.shape, dim) or (out.numel() and out.stride(-1) != 1) or (out.dim() != 2 and not out.is_contiguous()):
-        raise ValueError(f"out must have shape {(*ids.shape, dim)}, contiguous (or 2-dimensional with contiguous rows)")
+    if out.shape != shape or not _rows_contiguous(out):
+        raise ValueError(f"out must have shape {shape}, contiguous (or 2-dimensional with contiguous rows)")
     return out
 
 
-def _out_ld(out: torch.Tensor, dim: int) -> int:
-    return out.stride(0) if out.dim() == 2 and out.shape[0] > 1 else dim
+def _pitch(t: torch.Tensor, width: int) -> int:
+    """Elements from one row of a 2-dimensional (else contiguous) tensor to the next."""
+    return t.stride(0) if t.dim() == 2 else width
+
+
+def _rows_contiguous(t: torch.Tensor) -> bool:
+    return t.is_contiguous() or (t.dim() == 2 and (t.numel() == 0 or t.stride(1) == 1))
 
 
 def embed_lanes(dl: DeviceLanes, ids: torch.Tensor, dim: int, scale: float = 1.0, first: int = 0,
@@ -693,10 +694,11 @@ def embed_lanes(dl: DeviceLanes, ids: torch.Tensor, dim: int, scale: float = 1.0
         rows = (dl.n - first) // dim if dim > 0 else 0
     with _On(dev, stream) as sh:
         out = _embed_out(ids, dim, out, dev)
-        scope = LanesScope(_ptr(dl.stream), _ptr(dl.mant), _ptr(dl.lut), _ptr(dl.chunk_bits), _ptr(dl.group_start),
-                           ctypes.pointer(dl.table), ctypes.pointer(dl.info))
-        _check(lib().dfw_embed_lanes(ctypes.byref(scope), first, rows, dim, ids.data_ptr(), int(ids.dtype == torch.int64),
-                                     ids.numel(), scale, out.data_ptr(), _out_ld(out, dim), sh), "dfw_embed_lanes")
+        scope = LanesScope(dl.stream.data_ptr(), dl.mant.data_ptr(), dl.lut.data_ptr(), dl.chunk_bits.data_ptr(),
+                           dl.group_start.data_ptr(), ctypes.pointer(dl.table), ctypes.pointer(dl.info))
+        _check(lib().dfw_embed_lanes(ctypes.byref(scope), first, rows, dim, ids.data_ptr(), ids.dtype == torch.int64,
+                                     ids.numel(), scale, out.data_ptr(), _pitch(out, dim), sh),
+               "dfw_embed_lanes")
     return out
 
 
@@ -709,9 +711,9 @@ def embed_rows(table: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, out: 
     rows, dim = table.shape
     with _On(dev, stream) as sh:
         out = _embed_out(ids, dim, out, dev)
-        _check(lib().dfw_embed_rows(table.data_ptr(), rows, dim, _ld(table, dim), ids.data_ptr(),
-                                    int(ids.dtype == torch.int64), ids.numel(), scale, out.data_ptr(),
-                                    _out_ld(out, dim), sh), "dfw_embed_rows")
+        _check(lib().dfw_embed_rows(table.data_ptr(), rows, dim, table.stride(0), ids.data_ptr(), ids.dtype == torch.int64,
+                                    ids.numel(), scale, out.data_ptr(), _pitch(out, dim), sh),
+               "dfw_embed_rows")
     return out
 
 
@@ -724,14 +726,12 @@ def embed_grad(ids: torch.Tensor, dy: torch.Tensor, rows: int, scale: float = 1.
     ``accumulate`` it is added to ``out``, and rows without tokens stay as they
     are.  ``scratch`` (uint8, ``embed_grad_scratch_bytes``) may be passed to
     reuse one buffer; calls that overlap in time need one each."""
-    dev = dy.device
+    dev, shape = dy.device, dy.shape
     _expect("dy", dy, dev, _FLOATS)
     _expect("ids", ids, dev, _IDS)
-    if dy.dim() != ids.dim() + 1 or dy.shape[:-1] != ids.shape or not ids.is_contiguous():
-        raise ValueError("dy must have one row per id, ids must be contiguous")
-    if (dy.numel() and dy.stride(-1) != 1) or (dy.dim() != 2 and not dy.is_contiguous()):
-        raise ValueError("dy must be contiguous (or 2-dimensional with contiguous rows)")
-    tokens, dim = ids.numel(), dy.shape[-1]
+    if len(shape) == 0 or shape[:-1] != ids.shape or not ids.is_contiguous() or not _rows_contiguous(dy):
+        raise ValueError("dy must have one contiguous row per id, ids must be contiguous")
+    tokens, dim = ids.numel(), shape[-1]
     with _On(dev, stream) as sh:
         if out is None:
             if accumulate:
@@ -744,13 +744,14 @@ def embed_grad(ids: torch.Tensor, dy: torch.Tensor, rows: int, scale: float = 1.
             if out.shape != (rows, dim) or not out.is_contiguous():
                 raise ValueError(f"out must be a contiguous [{rows}, {dim}] tensor")
         if scratch is None:
-            scratch = torch.empty(embed_grad_scratch_bytes(tokens, dim), dtype=torch.uint8, device=dev)
+            need = embed_grad_scratch_bytes(tokens, dim)
+            scratch = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
         else:
             _expect("scratch", scratch, dev, _BYTES, 1)
-        _check(lib().dfw_embed_grad(ids.data_ptr(), int(ids.dtype == torch.int64), tokens, dy.data_ptr(),
-                                    int(dy.dtype == torch.float32), _out_ld(dy, dim), rows, dim, scale, out.data_ptr(),
-                                    int(out.dtype == torch.float32), int(accumulate), scratch.data_ptr(),
-                                    scratch.numel(), sh), "dfw_embed_grad")
+        _check(lib().dfw_embed_grad(ids.data_ptr(), ids.dtype == torch.int64, tokens, dy.data_ptr(), dy.dtype == torch.float32,
+                                    _pitch(dy, dim), rows, dim, scale, out.data_ptr(),
+                                    out.dtype == torch.float32, accumulate, None if scratch is None else scratch.data_ptr(),
+                                    0 if scratch is None else scratch.numel(), sh), "dfw_embed_grad")
     return out
 
 

@@ -1047,7 +1047,7 @@ GradCut grad_cut(uint64_t tokens, uint32_t dim) {
 }
 
 uint64_t embed_grad_scratch(uint64_t tokens, uint32_t dim) {
-    if (tokens == 0u) return 0u;
+    if (tokens <= GRAD_FEW) return 0u;
     const GradCut c = grad_cut(tokens, dim);
     return c.joins + c.list * (c.blocks > 1u ? 4u : 2u) + (c.windows > 1u ? (uint64_t)c.windows * 2u * dim * 4u : 0u);
 }
@@ -1102,7 +1102,8 @@ dfw_status launch_embed_grad(const void *d_ids, int ids64, uint64_t tokens, cons
     SortParams sp;
     dfw_status st = ids_checked(d_ids, ids64, tokens, rows, sp.ids);
     if (st != DFW_OK) return st;
-    if (dim < 1u || dim > DFW_EMBED_MAX_DIM || !d_grad || (tokens && (!d_dy || !d_scratch)) || (tokens > 1u && ld_dy < dim) ||
+    if (dim < 1u || dim > DFW_EMBED_MAX_DIM || !d_grad || (tokens && !d_dy) || (tokens > GRAD_FEW && !d_scratch) ||
+        (tokens > 1u && ld_dy < dim) ||
         (dy_fp32 | grad_fp32 | accumulate) & ~1)
         return DFW_EINVAL;
     if ((reinterpret_cast<uintptr_t>(d_dy) & (dy_fp32 ? 3u : 1u)) || (reinterpret_cast<uintptr_t>(d_grad) & (grad_fp32 ? 3u : 1u)) ||

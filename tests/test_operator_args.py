@@ -125,9 +125,10 @@ def test_embed_rows_refuses():
 
 def test_embed_grad_refuses():
     lib = dfw.lib()
-    need = dfw.embed_grad_scratch_bytes(7, 64)
+    need = dfw.embed_grad_scratch_bytes(200, 64)
+    assert need > 0 and dfw.embed_grad_scratch_bytes(7, 64) == 0  # few tokens need none
 
-    def call(ids=A, wide=1, tokens=7, dy=A, dyf=1, ld=64, rows=9, dim=64, grad=A, gf=1, acc=0, scratch=A, nbytes=need):
+    def call(ids=A, wide=1, tokens=200, dy=A, dyf=1, ld=64, rows=9, dim=64, grad=A, gf=1, acc=0, scratch=A, nbytes=need):
         return lib.dfw_embed_grad(ids, wide, tokens, dy, dyf, ld, rows, dim, 1.0, grad, gf, acc, scratch, nbytes, None)
 
     assert call(ids=None) == call(dy=None) == call(grad=None) == call(scratch=None) == dfw.EINVAL
