@@ -641,12 +641,15 @@ q4_fn q4_variant(const Q4Params &q, int nt, uint32_t warps, bool split) {
 
 dfw_status launch_q4_pass(Q4GemvParams a, int dev, int sms, cudaStream_t s) {
     const int nt = a.m > 8u ? 2 : 1;
-    // as few CTAs to a row tile as their shared memory allows, then as many warps
+    // as few CTAs to a row tile as their shared memory allows, then as many
+    // warps, but 16 where a CTA has fewer than 256 tiles (4096 x 4096, 64 tiles:
+    // 5.96 us with 16, 6.25 with 32; 65536 x 4096, 886 tiles: 30.9 and 29.4)
+    const uint64_t row_share = (a.q.row_tiles + (uint64_t)sms - 1u) / (uint64_t)sms;
     uint32_t split = 1, warps = 0, smem = 0;
     for (; split <= 8u && !warps; split *= 2u) {
         const uint32_t tiles = (a.q.col_tiles + split - 1u) / split;
         a.pitch = tiles * 2u * Q4_COLS + 64u;  // neighbouring vectors 16 banks apart
-        for (uint32_t w = nt == 1 ? 32u : 16u; w >= 16u && !warps; w -= 16u) {
+        for (uint32_t w = nt == 1 && row_share * tiles >= 256u ? 32u : 16u; w >= 16u && !warps; w -= 16u) {
             smem = w * (q4_ring(nt, w) * Q4_STEP * a.q.tile_bytes + 64u * a.m) + a.m * a.pitch + (split > 1u ? Q4_JOIN_BYTES : 0u);
             if (smem <= SMEM_MOST) warps = w;
         }
