@@ -384,6 +384,7 @@ __global__ void __launch_bounds__(256) embed_single_rows(const RowsOfLanes p) {
 // remote writes of neighbouring lanes are then neighbours too (writing every
 // token straight to its place measured 4 times as long at 65536 tokens).
 // Tokens without a row get key `rows` and end up behind all others.
+// PACK: key and place within the block fit 16 bits each and travel as one word.
 constexpr uint32_t SORT_THREADS = 1024, SORT_WARPS = 32, SORT_STRIDE = 257;
 
 struct SortParams {
@@ -393,12 +394,12 @@ struct SortParams {
     uint32_t passes, bits;  // digits of a key and their width, at most 8
 };
 
-template <int C, int IPT>
+template <int C, int IPT, bool PACK>
 constexpr uint32_t sort_smem() {
-    return SORT_WARPS * SORT_STRIDE * 4u + (256u + 256u + 32u) * 4u + SORT_THREADS * IPT * 8u * (C > 1 ? 2u : 1u);
+    return SORT_WARPS * SORT_STRIDE * 4u + (256u + 256u + 32u) * 4u + SORT_THREADS * IPT * (PACK ? 4u : 8u) * (C > 1 ? 2u : 1u);
 }
 
-template <int C, int IPT>
+template <int C, int IPT, bool PACK>
 __global__ void __launch_bounds__(SORT_THREADS, 1) grad_sort(const SortParams p) {
     constexpr uint32_t CAP = SORT_THREADS * IPT;
     extern __shared__ __align__(16) uint8_t smem[];
@@ -406,22 +407,28 @@ __global__ void __launch_bounds__(SORT_THREADS, 1) grad_sort(const SortParams p)
     uint32_t *total = cnt + SORT_WARPS * SORT_STRIDE;    // this CTA's count of each digit
     uint32_t *shift_by = total + 256;                    // from a digit's place in this CTA's order to the cluster's
     uint32_t *sums = shift_by + 256;
-    uint32_t *s_key = sums + 32, *s_pos = s_key + CAP;            // this CTA's part of the order
-    uint32_t *l_key = C > 1 ? s_pos + CAP : s_key, *l_pos = l_key + CAP;  // this CTA's tokens in digit order
+    constexpr uint32_t WORDS = PACK ? CAP : 2u * CAP;
+    uint32_t *s_key = sums + 32, *s_pos = s_key + CAP;                             // this CTA's part of the order
+    uint32_t *l_key = C > 1 ? s_key + WORDS : s_key, *l_pos = l_key + CAP;  // this CTA's tokens in digit order
     const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
     const uint32_t rank = blockIdx.x % C, base = blockIdx.x * CAP, run = warp * 32u * IPT + lane;
     griddep_launch_dependents();
     if (blockIdx.x == 0u && tid < 2u) p.joins[tid] = 0u;
-    uint32_t key[IPT], pos[IPT];
+    const uint32_t block = base - rank * CAP;  // the cluster's first token
+    uint32_t key[IPT], pos[PACK ? 1 : IPT];  // PACK: key[j] holds both
 #pragma unroll
     for (int j = 0; j < IPT; ++j) {
         uint64_t row = p.ids.rows;
-        pos[j] = base + run + 32u * j;
+        const uint32_t t = base + run + 32u * j;
         key[j] = 0xFFFFFFFFu;  // behind every token
-        if (pos[j] < p.ids.tokens) key[j] = token_row(p.ids, pos[j], row, true) ? (uint32_t)row : (uint32_t)p.ids.rows;
+        if (t < p.ids.tokens) {
+            key[j] = token_row(p.ids, t, row, true) ? (uint32_t)row : (uint32_t)p.ids.rows;
+            if constexpr (PACK) key[j] = key[j] << 16 | (t - block);
+        }
+        if constexpr (!PACK) pos[j] = t;
     }
     for (uint32_t pass = 0; pass < p.passes; ++pass) {
-        const uint32_t shift = p.bits * pass, mask = (1u << p.bits) - 1u;
+        const uint32_t shift = p.bits * pass + (PACK ? 16u : 0u), mask = (1u << p.bits) - 1u;
         for (uint32_t i = lane; i < 256u; i += 32u) cnt[warp * SORT_STRIDE + i] = 0u;
         __syncwarp();
         uint32_t at[IPT];
@@ -486,7 +493,7 @@ __global__ void __launch_bounds__(SORT_THREADS, 1) grad_sort(const SortParams p)
         for (int j = 0; j < IPT; ++j) {
             const uint32_t to = cnt[warp * SORT_STRIDE + ((key[j] >> shift) & mask)] + at[j];
             l_key[to] = key[j];
-            l_pos[to] = pos[j];
+            if constexpr (!PACK) l_pos[to] = pos[j];
         }
         if constexpr (C > 1) {
             cluster_sync();  // every CTA's counts are out, and its part of the last order has been read
@@ -507,7 +514,7 @@ __global__ void __launch_bounds__(SORT_THREADS, 1) grad_sort(const SortParams p)
                 const uint32_t from = run + 32u * j, k = l_key[from];
                 const uint32_t to = from + shift_by[(k >> shift) & mask], r = to / CAP, i = to % CAP;
                 st_cluster(map_rank(smem_u32(s_key + i), r), k);
-                st_cluster(map_rank(smem_u32(s_pos + i), r), l_pos[from]);
+                if constexpr (!PACK) st_cluster(map_rank(smem_u32(s_pos + i), r), l_pos[from]);
             }
             cluster_sync();
         } else {
@@ -516,7 +523,7 @@ __global__ void __launch_bounds__(SORT_THREADS, 1) grad_sort(const SortParams p)
 #pragma unroll
         for (int j = 0; j < IPT; ++j) {
             key[j] = s_key[run + 32u * j];
-            pos[j] = s_pos[run + 32u * j];
+            if constexpr (!PACK) pos[j] = s_pos[run + 32u * j];
         }
         if constexpr (C == 1) __syncthreads();  // before the next pass writes
     }
@@ -524,8 +531,8 @@ __global__ void __launch_bounds__(SORT_THREADS, 1) grad_sort(const SortParams p)
     for (int j = 0; j < IPT; ++j) {
         const uint32_t t = base + run + 32u * j;
         if (t < p.ids.tokens) {
-            p.keys[t] = key[j];
-            p.pos[t] = pos[j];
+            p.keys[t] = PACK ? key[j] >> 16 : key[j];
+            p.pos[t] = PACK ? block + (key[j] & 0xFFFFu) : pos[PACK ? 0 : j];
         }
     }
 }
@@ -776,12 +783,15 @@ __global__ void __launch_bounds__(256) grad_join(const ReduceParams p) {
     for (uint64_t item = blockIdx.x; item < (uint64_t)many * narrow; item += gridDim.x) {
         const uint32_t w = p.joins[4u + p.windows + (uint32_t)(item / narrow)];
         const uint32_t col = (uint32_t)(item % narrow) * 32u * VEC + lane * VEC, key = __ldg(p.keys + (uint64_t)(w + 1u) * p.window);
-        uint32_t last = w + JOIN_FEW;  // the last window that begins with the row, 32 windows at a look
-        for (;;) {
-            const uint64_t t = (uint64_t)(last + 1u + lane) * p.window;
-            const uint32_t m = __ballot_sync(0xFFFFFFFFu, t < p.tokens && __ldg(p.keys + min(t, (uint64_t)p.tokens - 1u)) == key);
-            last += m == 0xFFFFFFFFu ? 32u : __ffs(~m) - 1u;
-            if (m != 0xFFFFFFFFu) break;
+        // the last window that begins with the row: the windows that do come
+        // first, so 32 probes at a time narrow it down
+        uint32_t last = w + JOIN_FEW, over = p.windows;
+        while (over - last > 1u) {
+            const uint32_t step = (over - last + 31u) / 32u;
+            const uint64_t probe = (uint64_t)last + (uint64_t)step * (lane + 1u);
+            const uint32_t m = __ballot_sync(0xFFFFFFFFu, probe < over && __ldg(p.keys + (probe < over ? probe : w) * p.window) == key);
+            last += step * __popc(m);
+            over = min(over, last + step);
         }
         float sum[VEC] = {};
         if (col < p.dim) {
@@ -798,7 +808,10 @@ __global__ void __launch_bounds__(256) grad_join(const ReduceParams p) {
             for (uint32_t k = 1; k < 8u; ++k) sum[j] += s_sum[k][lane * VEC + j];
         put_row<OUT, VEC>(p.grad, (uint64_t)key * p.dim + col, sum, p.scale, p.accumulate != 0u);
     }
-    for (uint64_t item = blockIdx.x; item < (uint64_t)few * wide; item += gridDim.x) {
+    // (CTAs without an item of the first list begin here)
+    const uint32_t busy = (uint32_t)((uint64_t)many * narrow % gridDim.x);
+    for (uint64_t item = blockIdx.x >= busy ? blockIdx.x - busy : blockIdx.x + gridDim.x - busy; item < (uint64_t)few * wide;
+         item += gridDim.x) {
         const uint32_t entry = p.joins[4u + (uint32_t)(item / wide)], w = entry & 0xFFFFFFu, more = entry >> 24;
         const uint32_t col = ((uint32_t)(item % wide) * 256u + threadIdx.x) * VEC;
         if (col >= p.dim) continue;
@@ -1052,17 +1065,25 @@ uint64_t embed_grad_scratch(uint64_t tokens, uint32_t dim) {
     return c.joins + c.list * (c.blocks > 1u ? 4u : 2u) + (c.windows > 1u ? (uint64_t)c.windows * 2u * dim * 4u : 0u);
 }
 
-template <int C, int IPT>
+template <int C, int IPT, bool PACK>
 dfw_status launch_grad_sort(const SortParams &p, uint32_t blocks, cudaStream_t s) {
     static int opted[16];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 16) return DFW_ECUDA;
+    constexpr uint32_t smem = sort_smem<C, IPT, PACK>();
     if (!opted[dev]) {
-        if (cudaFuncSetAttribute(grad_sort<C, IPT>, cudaFuncAttributeMaxDynamicSharedMemorySize, sort_smem<C, IPT>()) != cudaSuccess)
+        if (cudaFuncSetAttribute(grad_sort<C, IPT, PACK>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
             return DFW_ECUDA;
         opted[dev] = 1;
     }
-    return launch_with(grad_sort<C, IPT>, blocks * C, SORT_THREADS, sort_smem<C, IPT>(), false, C, s, p);
+    return launch_with(grad_sort<C, IPT, PACK>, blocks * C, SORT_THREADS, smem, false, C, s, p);
+}
+template <bool PACK>
+dfw_status launch_grad_sort(const SortParams &p, const GradCut &cut, cudaStream_t s) {
+    if (cut.ctas == 1u) return launch_grad_sort<1, 1, PACK>(p, cut.blocks, s);
+    if (cut.ipt == 1u) return launch_grad_sort<8, 1, PACK>(p, cut.blocks, s);
+    if (cut.ipt == 4u) return launch_grad_sort<8, 4, PACK>(p, cut.blocks, s);
+    return launch_grad_sort<8, 8, PACK>(p, cut.blocks, s);
 }
 
 template <typename DY, typename OUT, int V>
@@ -1135,10 +1156,7 @@ dfw_status launch_embed_grad(const void *d_ids, int ids64, uint64_t tokens, cons
     while (rows >> key_bits) ++key_bits;  // keys go up to `rows`
     sp.passes = (key_bits + 7u) / 8u;
     sp.bits = (key_bits + sp.passes - 1u) / sp.passes;
-    st = cut.ctas == 1u ? launch_grad_sort<1, 1>(sp, cut.blocks, s)
-         : cut.ipt == 1u ? launch_grad_sort<8, 1>(sp, cut.blocks, s)
-         : cut.ipt == 4u ? launch_grad_sort<8, 4>(sp, cut.blocks, s)
-                         : launch_grad_sort<8, 8>(sp, cut.blocks, s);
+    st = key_bits <= 16u ? launch_grad_sort<true>(sp, cut, s) : launch_grad_sort<false>(sp, cut, s);
     if (st != DFW_OK) return st;
     if (fill_bytes && (st = launch_with(grad_zero, fillers, 512, 0, true, 1, s, fill, fill_bytes)) != DFW_OK) return st;
     ReduceParams p;
