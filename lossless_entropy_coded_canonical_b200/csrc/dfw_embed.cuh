@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(NT) embed_lanes_rows(const RowsOfLanes p) {
 #pragma unroll
                 for (uint32_t j = 0; j < 4u; ++j) {
                     const uint64_t w = g0 + 512u * j + 16u * lane;
-                    if (w < cur.w0 || w >= end) continue;
+                    if (w < cur.w0 || w >= end || !check(w + V <= end, CK_EMBED_STORE)) continue;
                     uint4 a, b;
                     join16(mrow + 512u * j, erow + 32u * j, a, b);
                     stg256_cs(out + (w - cur.w0), scaled8(a, p.scale, one), scaled8(b, p.scale, one));
@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(NT) embed_lanes_rows(const RowsOfLanes p) {
                 for (uint32_t j = 0; j < 8u; ++j) {  // piece lane + 32 j: words 2 (piece mod 8) and + 1 of chunk piece / 8
                     const uint32_t piece = lane + 32u * j;
                     const uint64_t w = g0 + 8u * piece;
-                    if (w < cur.w0 || w >= end) continue;
+                    if (w < cur.w0 || w >= end || !check(w + V <= end, CK_EMBED_STORE)) continue;
                     const uint32_t e = exps0 + 4u * (piece >> 3) + 2u * EXP_STRIDE * (piece & 7u), m = smem_u32(mbuf) + 8u * piece;
                     uint4 v;
                     join4(lds32(e), lds32(m), v.x, v.y);
@@ -492,6 +492,7 @@ __global__ void __launch_bounds__(SORT_THREADS, 1) grad_sort(const SortParams p)
 #pragma unroll
         for (int j = 0; j < IPT; ++j) {
             const uint32_t to = cnt[warp * SORT_STRIDE + ((key[j] >> shift) & mask)] + at[j];
+            if (!check(to < CAP, CK_GRAD_SORT)) continue;
             l_key[to] = key[j];
             if constexpr (!PACK) l_pos[to] = pos[j];
         }
@@ -513,6 +514,7 @@ __global__ void __launch_bounds__(SORT_THREADS, 1) grad_sort(const SortParams p)
             for (int j = 0; j < IPT; ++j) {
                 const uint32_t from = run + 32u * j, k = l_key[from];
                 const uint32_t to = from + shift_by[(k >> shift) & mask], r = to / CAP, i = to % CAP;
+                if (!check(r < C, CK_GRAD_SORT)) continue;
                 st_cluster(map_rank(smem_u32(s_key + i), r), k);
                 if constexpr (!PACK) st_cluster(map_rank(smem_u32(s_pos + i), r), l_pos[from]);
             }
@@ -591,7 +593,7 @@ __global__ void __launch_bounds__(256) grad_merge(const MergeParams p) {
     }
 #pragma unroll
     for (int d = 1; d < LANES; d <<= 1) place += __shfl_xor_sync(0xFFFFFFFFu, place, d);
-    if (sub == 0u && i < p.tokens) {
+    if (sub == 0u && i < p.tokens && check(place < p.tokens, CK_GRAD_SORT)) {
         p.out_keys[place] = key;
         p.out_pos[place] = __ldg(p.pos + t);
     }
@@ -664,9 +666,11 @@ struct Raw<__nv_bfloat16, 8> {
     }
 };
 
-// Writes (or adds) scale x sum to VEC columns of a row, rounded once.
+// Writes (or adds) scale x sum to VEC columns of a row, rounded once; `size` is
+// the gradient's, for the checks build.
 template <typename OUT, int VEC>
-__device__ __forceinline__ void put_row(void *grad, uint64_t at, const float (&acc)[VEC], float scale, bool add) {
+__device__ __forceinline__ void put_row(void *grad, uint64_t at, const float (&acc)[VEC], float scale, bool add, uint64_t size) {
+    if (!check(at + VEC <= size, CK_GRAD_STORE)) return;
     constexpr int N = VEC * sizeof(OUT) > 16 ? 16 / sizeof(OUT) : VEC;  // at most 16 bytes at once
 #pragma unroll
     for (int i = 0; i < VEC; i += N) {
@@ -713,8 +717,8 @@ __global__ void __launch_bounds__(128, 6) grad_reduce(const ReduceParams p) {
                 on = on && t < p.tokens && __ldg(p.keys + min(t, (uint64_t)p.tokens - 1u)) == tail;
                 more += on;
             }
-            if (more < JOIN_FEW) p.joins[4u + atomicAdd(p.joins, 1u)] = w | more << 24;
-            else p.joins[4u + p.windows + atomicAdd(p.joins + 1, 1u)] = w;
+            const uint32_t at = atomicAdd(p.joins + (more < JOIN_FEW ? 0 : 1), 1u);
+            if (check(at < p.windows, CK_GRAD_PARTIAL)) p.joins[4u + (more < JOIN_FEW ? 0u : p.windows) + at] = more < JOIN_FEW ? w | more << 24 : w;
         }
     }
     const DY *dy = static_cast<const DY *>(p.dy) + col;
@@ -725,6 +729,7 @@ __global__ void __launch_bounds__(128, 6) grad_reduce(const ReduceParams p) {
         if (cur >= p.rows) return;
         const bool left = first && cur == prev, right = last && cur == next;
         if (left || right) {
+            if (!check(p.windows > 1u && w < p.windows && col + VEC <= p.dim, CK_GRAD_PARTIAL)) return;
             float *dst = p.partial + ((uint64_t)w * 2u + (left ? 0u : 1u)) * p.dim + col;
             constexpr int N = VEC > 4 ? 4 : VEC;
 #pragma unroll
@@ -735,14 +740,14 @@ __global__ void __launch_bounds__(128, 6) grad_reduce(const ReduceParams p) {
                 *reinterpret_cast<Pack<float, N> *>(dst + k) = o;
             }
         } else {
-            put_row<OUT, VEC>(p.grad, (uint64_t)cur * p.dim + col, acc, p.scale, p.accumulate != 0u);
+            put_row<OUT, VEC>(p.grad, (uint64_t)cur * p.dim + col, acc, p.scale, p.accumulate != 0u, (uint64_t)p.rows * p.dim);
         }
     };
     for (uint32_t i = 0; i < n; i += U) {  // window is a multiple of U: keys past the last token read as no row
         Raw<DY, VEC> v[U];
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (keys[i + u] < p.rows) v[u] = *reinterpret_cast<const Raw<DY, VEC> *>(dy + (uint64_t)pos[i + u] * p.ld_dy);
+            if (keys[i + u] < p.rows && check(pos[i + u] < p.tokens, CK_GRAD_READ)) v[u] = *reinterpret_cast<const Raw<DY, VEC> *>(dy + (uint64_t)pos[i + u] * p.ld_dy);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const uint32_t key = keys[i + u];
@@ -806,7 +811,7 @@ __global__ void __launch_bounds__(256) grad_join(const ReduceParams p) {
 #pragma unroll
         for (int j = 0; j < VEC; ++j)
             for (uint32_t k = 1; k < 8u; ++k) sum[j] += s_sum[k][lane * VEC + j];
-        put_row<OUT, VEC>(p.grad, (uint64_t)key * p.dim + col, sum, p.scale, p.accumulate != 0u);
+        put_row<OUT, VEC>(p.grad, (uint64_t)key * p.dim + col, sum, p.scale, p.accumulate != 0u, (uint64_t)p.rows * p.dim);
     }
     // (CTAs without an item of the first list begin here)
     const uint32_t busy = (uint32_t)((uint64_t)many * narrow % gridDim.x);
@@ -827,7 +832,7 @@ __global__ void __launch_bounds__(256) grad_join(const ReduceParams p) {
 #pragma unroll
             for (int j = 0; j < VEC; ++j) sum[j] += k <= more ? v[k - 1u].v[j] : 0.f;
         }
-        put_row<OUT, VEC>(p.grad, (uint64_t)key * p.dim + col, sum, p.scale, p.accumulate != 0u);
+        put_row<OUT, VEC>(p.grad, (uint64_t)key * p.dim + col, sum, p.scale, p.accumulate != 0u, (uint64_t)p.rows * p.dim);
     }
 }
 
@@ -911,7 +916,7 @@ __global__ void __launch_bounds__(256) grad_few(const FewParams p) {
             for (int k = 0; k < VEC; ++k) acc[k] += v[u].get(k);
             const uint32_t r = s_row2[i + u];
             if (i + u + 1u < n && s_row2[i + u + 1u] == r) continue;
-            put_row<OUT, VEC>(p.grad, (uint64_t)r * p.dim + col, acc, p.scale, p.accumulate != 0u);
+            put_row<OUT, VEC>(p.grad, (uint64_t)r * p.dim + col, acc, p.scale, p.accumulate != 0u, p.ids.rows * p.dim);
 #pragma unroll
             for (int k = 0; k < VEC; ++k) acc[k] = 0.f;
         }

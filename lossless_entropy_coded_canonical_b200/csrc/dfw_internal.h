@@ -74,6 +74,14 @@ enum CheckSite : uint32_t {
     CK_CLOSED_READ = 17,        // a closed-form decode read past the stream
     CK_EMBED_COPY = 18,         // an embedding row's group copied beyond its buffers or slot
     CK_EMBED_READ = 19,         // an embedding row's stream reads or exponent slots past their areas
+    CK_EMBED_STORE = 20,        // an embedding row written past its width
+    CK_Q4_COPY = 21,            // a 4-bit tile copied from beyond the packed matrix or into another warp's ring
+    CK_Q4_SUMS = 22,            // a product's sums beyond their shared areas
+    CK_Q4_STORE = 23,           // a product stored beyond its vector
+    CK_GRAD_SORT = 24,          // a token sorted to a place beyond its block or list
+    CK_GRAD_READ = 25,          // a gradient row read beyond the tokens
+    CK_GRAD_PARTIAL = 26,       // a partial sum or join entry beyond its list
+    CK_GRAD_STORE = 27,         // a gradient stored beyond the table
 };
 
 // A named range on profiler timelines (NVTX) for the duration of a call;

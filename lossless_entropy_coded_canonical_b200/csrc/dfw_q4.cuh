@@ -383,7 +383,7 @@ __device__ __forceinline__ void q4_tile_products(const Q4Tile<GT, Z> &b, uint32_
 }
 
 __device__ __forceinline__ void q4_store(const Q4GemvParams &a, uint64_t row, uint32_t col, float v) {
-    if (row >= a.q.rows) return;
+    if (row >= a.q.rows || !check(col < a.m, CK_Q4_STORE)) return;
     v *= 64.f;
     if (a.y_fp32) static_cast<float *>(a.y)[col * a.ldy + row] = v;
     else static_cast<__nv_bfloat16 *>(a.y)[col * a.ldy + row] = __float2bfloat16_rn(v);
@@ -416,6 +416,11 @@ __global__ void __launch_bounds__(32 * W, 1) q4_gemv_tiles(const Q4GemvParams a)
     auto next_slot = [&](uint32_t slot) {
         return RING == 2u ? slot ^ ring ^ (ring + SLOT) : slot + SLOT == ring + RING * SLOT ? ring : slot + SLOT;
     };
+    auto in_bounds = [&](uint32_t dst, const uint8_t *from) {  // of one 16-byte copy (checks build)
+        return check(from >= a.packed && from + 16u <= a.packed + a.q.row_tiles * a.q.col_tiles * TILE &&
+                         dst >= smem_u32(smem) + warp * RING * SLOT && dst + 16u <= smem_u32(smem) + (warp + 1u) * RING * SLOT,
+                     CK_Q4_COPY);
+    };
     auto fetch = [&]() {
         while (in_left == 0u && in_row < rows && cts) {  // the next pass
             const uint32_t n = min(a.pass, rows - in_row), lo = first(warp, n);
@@ -427,7 +432,7 @@ __global__ void __launch_bounds__(32 * W, 1) q4_gemv_tiles(const Q4GemvParams a)
         if (in_left >= Q4_STEP && (!SPLIT || in_ct + Q4_STEP <= cts)) {  // a whole step, contiguous
 #pragma unroll
             for (uint32_t at = 0; at < SLOT; at += 512u)
-                if (at + 512u <= SLOT || lane < (SLOT - at) / 16u) cp_async16(slot_in + at, src + at);
+                if ((at + 512u <= SLOT || lane < (SLOT - at) / 16u) && in_bounds(slot_in + at, src + at)) cp_async16(slot_in + at, src + at);
             src += SLOT;
             in_left -= Q4_STEP;
             in_ct += Q4_STEP;
@@ -438,9 +443,9 @@ __global__ void __launch_bounds__(32 * W, 1) q4_gemv_tiles(const Q4GemvParams a)
         } else {
             for (uint32_t u = 0; u < Q4_STEP && in_left; ++u) {
                 const uint32_t dst = slot_in + u * TILE;
-                cp_async16(dst, src);
-                cp_async16(dst + 512u, src + 512);
-                if (lane < (TILE - Q4_CODES) / 16u) cp_async16(dst + Q4_CODES, src + Q4_CODES);
+                if (in_bounds(dst, src)) cp_async16(dst, src);
+                if (in_bounds(dst + 512u, src + 512)) cp_async16(dst + 512u, src + 512);
+                if (lane < (TILE - Q4_CODES) / 16u && in_bounds(dst + Q4_CODES, src + Q4_CODES)) cp_async16(dst + Q4_CODES, src + Q4_CODES);
                 src += TILE;
                 if (SPLIT && ++in_ct == cts) {
                     in_ct = 0;
@@ -481,6 +486,7 @@ __global__ void __launch_bounds__(32 * W, 1) q4_gemv_tiles(const Q4GemvParams a)
     float acc[NT][4] = {};
     uint32_t slot = ring;
     auto put_away = [&](uint32_t row) {
+        if (!check(warp + row < W + a.pass - 1u, CK_Q4_SUMS)) return;
         float *p = sums + (warp + row) * outs;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -527,7 +533,7 @@ __global__ void __launch_bounds__(32 * W, 1) q4_gemv_tiles(const Q4GemvParams a)
                 for (uint32_t w = w0; w < w1; ++w) v += sums[(w + r) * outs + o];
             }
             if constexpr (!SPLIT) q4_store(a, (uint64_t)Q4_ROWS * (rt0 + done + r) + (o & 15u), o >> 4, v);
-            else st_cluster_f32(map_rank(smem_u32(join + ((r / split) * split + rank) * outs + o), r % split), v);
+            else if (check((((r / split) * split + rank) * outs + o) * 4u < Q4_JOIN_BYTES, CK_Q4_SUMS)) st_cluster_f32(map_rank(smem_u32(join + ((r / split) * split + rank) * outs + o), r % split), v);
         }
         if constexpr (SPLIT) {  // row tile r of the pass is added up by CTA r mod split
             cluster_sync();

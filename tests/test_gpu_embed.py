@@ -284,6 +284,27 @@ def test_gradient_of_whole_numbers_is_exact(rows, dim, tokens, spread):
         assert torch.equal(dfw.embed_grad(ids.cuda(), d, rows, scale=2.0).double().cpu(), want)
 
 
+@pytest.mark.parametrize("tokens", [128, 129, 1024, 1025, 8192, 8193, 16385, 32768, 32769, 65536, 65537, 131073, 140000])
+@pytest.mark.parametrize("rows", [90, 65535, 65536])
+def test_gradient_at_every_change_of_its_cut(rows, tokens):
+    """The sizes where the launches, blocks, windows and the width of a sorted
+    token change, one token behind each, exact in whole numbers."""
+    ids = grad_ids(rows, tokens, "zipf", tokens)
+    ids[-1] = rows - 1
+    dy = torch.randint(-3, 4, (tokens, 8), generator=torch.Generator("cuda").manual_seed(5), device="cuda").float()
+    want, _, _ = grad_of(ids, dy, rows, 1.0)
+    assert torch.equal(dfw.embed_grad(ids.cuda(), dy.to(torch.bfloat16), rows).double().cpu(), want)
+
+
+def test_the_most_tokens_and_too_many():
+    ids = torch.full((1 << 20,), 3, dtype=torch.int32, device="cuda")
+    ids[: 1 << 19] = torch.arange(1 << 19, dtype=torch.int32, device="cuda") % 100000
+    dy = torch.ones(1 << 20, 1, dtype=torch.bfloat16, device="cuda")
+    assert torch.equal(dfw.embed_grad(ids, dy, 100000)[:, 0].cpu(), torch.bincount(ids.long().cpu(), minlength=100000).float())
+    with pytest.raises(dfw.DfwError):
+        dfw.embed_grad(ids.new_zeros((1 << 20) + 1), dy.new_ones((1 << 20) + 1, 1), 10)
+
+
 @pytest.mark.parametrize("rows,dim,tokens,spread", [(200, 48, 150, "any"), (50, 129, 5000, "zipf"), (300, 16, 1, "any"), (20, 8, 30, "pads")])
 def test_gradient_accumulates(rows, dim, tokens, spread):
     ids = grad_ids(rows, tokens, spread, 4)
