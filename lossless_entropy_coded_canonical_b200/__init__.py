@@ -526,40 +526,40 @@ def status_bits(stream=None) -> tuple[int, int]:
 
 # ------------------------------------------- 4-bit weights and embedding rows
 
-class _On:
-    """Makes a tensor's device current, and ``stream`` if one is given (so
-    that what the call allocates belongs to it), for one library call."""
-    __slots__ = ("ctx", "index")
+# These calls serve single tokens, where the host's share counts: a call that
+# runs on the current device's current stream (almost all do) finds the stream
+# without building an object, and anything else re-enters itself under a
+# context that makes its device and stream current.
 
-    def __init__(self, device: torch.device, stream):
-        self.index = device.index
-        if stream is not None:
-            if stream.device != device:
-                raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
-            self.ctx = torch.cuda.stream(stream)
-        else:
-            self.ctx = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+def _here(device: torch.device, stream) -> int | None:
+    """The current stream's handle if the call needs no other stream or device."""
+    if stream is None and torch._C._cuda_getDevice() == device.index:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    return None
 
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        return torch._C._cuda_getCurrentRawStream(self.index)  # current_stream() builds an object: 3 us more
 
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+def _there(device: torch.device, stream):
+    """Makes ``stream`` (so that what the call allocates belongs to it), or the
+    tensors' device, current."""
+    if stream is None:
+        return torch.cuda.device(device)
+    if stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+    return torch.cuda.stream(stream)
 
 
 def _expect(name: str, t: torch.Tensor, device: torch.device, dtypes, dim: int | None = None) -> None:
-    if t.device != device or device.type != "cuda":
+    if t.is_cuda and t.device == device and t.dtype in dtypes and (
+            dim is None or (t.dim() == dim and (t.is_contiguous() or t.numel() == 0 or t.stride(-1) == 1))):
+        return
+    if not t.is_cuda or t.device != device:
         raise ValueError(f"{name} must be on {device if device.type == 'cuda' else 'a CUDA device'}, not {t.device}")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
-    if dim is not None and (t.dim() != dim or (t.numel() and t.stride(-1) != 1)):
-        raise ValueError(f"{name} must have {dim} dimensions, the last one contiguous")
+    raise ValueError(f"{name} must have {dim} dimensions, the last one contiguous")
 
 
-_BF16, _F32 = (torch.bfloat16,), (torch.float32,)
+_BF16 = (torch.bfloat16,)
 _FLOATS, _IDS, _BYTES = (torch.bfloat16, torch.float32), (torch.int32, torch.int64), (torch.uint8,)
 
 
@@ -605,10 +605,13 @@ def q4_pack(codes: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor | Non
                 raise ValueError(f"{name} must be a contiguous [{rows}, {cols} / {group}] tensor")
     if not codes.is_contiguous():
         raise ValueError("codes must be contiguous")
-    with _On(dev, stream) as sh:
-        q = _q4_new(rows, cols, group, zeros is not None, dev)
-        _check(lib().dfw_q4_pack(codes.data_ptr(), scales.data_ptr(), None if zeros is None else zeros.data_ptr(),
-                                 ctypes.byref(q.info), q.packed.data_ptr(), sh), "dfw_q4_pack")
+    sh = _here(dev, stream)
+    if sh is None:
+        with _there(dev, stream):
+            return q4_pack(codes, scales, zeros, group)
+    q = _q4_new(rows, cols, group, zeros is not None, dev)
+    _check(lib().dfw_q4_pack(codes.data_ptr(), scales.data_ptr(), None if zeros is None else zeros.data_ptr(),
+                             ctypes.byref(q.info), q.packed.data_ptr(), sh), "dfw_q4_pack")
     return q
 
 
@@ -617,18 +620,24 @@ def q4_quantise(w: torch.Tensor, group: int = 128, zeros: bool = False, stream=N
     with a scale, and with ``zeros`` a zero point, per row and ``group``
     columns (``dfw_q4_quantise``)."""
     _expect("w", w, w.device, _BF16, 2)
-    with _On(w.device, stream) as sh:
-        q = _q4_new(w.shape[0], w.shape[1], group, zeros, w.device)
-        _check(lib().dfw_q4_quantise(w.data_ptr(), w.stride(0) if w.shape[0] > 1 else w.shape[1], ctypes.byref(q.info), q.packed.data_ptr(), sh),
-               "dfw_q4_quantise")
+    sh = _here(w.device, stream)
+    if sh is None:
+        with _there(w.device, stream):
+            return q4_quantise(w, group, zeros)
+    q = _q4_new(w.shape[0], w.shape[1], group, zeros, w.device)
+    _check(lib().dfw_q4_quantise(w.data_ptr(), w.stride(0) if w.shape[0] > 1 else w.shape[1], ctypes.byref(q.info),
+                                 q.packed.data_ptr(), sh), "dfw_q4_quantise")
     return q
 
 
 def q4_dequantise(q: Q4Weights, stream=None) -> torch.Tensor:
     """The bf16 matrix [rows, cols] that ``q`` stands for (``dfw_q4_dequantise``)."""
-    with _On(q.packed.device, stream) as sh:
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.packed.device)
-        _check(lib().dfw_q4_dequantise(q.packed.data_ptr(), ctypes.byref(q.info), out.data_ptr(), sh), "dfw_q4_dequantise")
+    sh = _here(q.packed.device, stream)
+    if sh is None:
+        with _there(q.packed.device, stream):
+            return q4_dequantise(q)
+    out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.packed.device)
+    _check(lib().dfw_q4_dequantise(q.packed.data_ptr(), ctypes.byref(q.info), out.data_ptr(), sh), "dfw_q4_dequantise")
     return out
 
 
@@ -643,20 +652,22 @@ def q4_gemv(q: Q4Weights, x: torch.Tensor, out: torch.Tensor | None = None, out_
     if nd not in (1, 2) or shape[-1] != cols:
         raise ValueError(f"x must be [tokens, {cols}] or [{cols}], not {list(shape)}")
     _expect("x", x, dev, _BF16, nd)
-    m = shape[0] if nd == 2 else 1
-    want = (m, rows) if nd == 2 else (rows,)
-    with _On(dev, stream) as sh:
-        if out is None:
-            if out_dtype not in _FLOATS:
-                raise TypeError(f"out_dtype {out_dtype}, expected one of {_FLOATS}")
-            out = torch.empty(want, dtype=out_dtype, device=dev)
-        else:
-            _expect("out", out, dev, _FLOATS, nd)
-            if out.shape != want:
-                raise ValueError(f"out must have shape {want}")
-        _check(lib().dfw_q4_gemv(q.packed.data_ptr(), ctypes.byref(info), m, x.data_ptr(),
-                                 x.stride(0) if m > 1 else cols, out.data_ptr(), int(out.dtype == torch.float32),
-                                 out.stride(0) if m > 1 else rows, sh), "dfw_q4_gemv")
+    sh = _here(dev, stream)
+    if sh is None:
+        with _there(dev, stream):
+            return q4_gemv(q, x, out, out_dtype)
+    m, want = (shape[0], (shape[0], rows)) if nd == 2 else (1, (rows,))
+    if out is None:
+        if out_dtype not in _FLOATS:
+            raise TypeError(f"out_dtype {out_dtype}, expected one of {_FLOATS}")
+        out = x.new_empty(want, dtype=out_dtype)
+    else:
+        _expect("out", out, dev, _FLOATS, nd)
+        if out.shape != want:
+            raise ValueError(f"out must have shape {want}")
+        out_dtype = out.dtype
+    _check(lib().dfw_q4_gemv(q.packed.data_ptr(), ctypes.byref(info), m, x.data_ptr(), x.stride(0) if m > 1 else cols,
+                             out.data_ptr(), out_dtype is torch.float32, out.stride(0) if m > 1 else rows, sh), "dfw_q4_gemv")
     return out
 
 
@@ -666,7 +677,7 @@ def _embed_out(ids: torch.Tensor, dim: int, out, dev) -> torch.Tensor:
         raise ValueError("ids must be contiguous")
     shape = (*ids.shape, dim)
     if out is None:
-        return torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        return ids.new_empty(shape, dtype=torch.bfloat16)
     _expect("out", out, dev, _BF16)
     if out.shape != shape or not _rows_contiguous(out):
         raise ValueError(f"out must have shape {shape}, contiguous (or 2-dimensional with contiguous rows)")
@@ -690,15 +701,17 @@ def embed_lanes(dl: DeviceLanes, ids: torch.Tensor, dim: int, scale: float = 1.0
     whole rows from ``first``).  ``ids``: int32 or int64, any shape, negative =
     padding (a zero row); returns bf16 [*ids.shape, dim]."""
     dev = dl.mant.device
+    sh = _here(dev, stream) if dl.mant.is_cuda else 0
+    if sh is None:
+        with _there(dev, stream):
+            return embed_lanes(dl, ids, dim, scale, first, rows, out)
     if rows is None:
         rows = (dl.n - first) // dim if dim > 0 else 0
-    with _On(dev, stream) as sh:
-        out = _embed_out(ids, dim, out, dev)
-        scope = LanesScope(dl.stream.data_ptr(), dl.mant.data_ptr(), dl.lut.data_ptr(), dl.chunk_bits.data_ptr(),
-                           dl.group_start.data_ptr(), ctypes.pointer(dl.table), ctypes.pointer(dl.info))
-        _check(lib().dfw_embed_lanes(ctypes.byref(scope), first, rows, dim, ids.data_ptr(), ids.dtype == torch.int64,
-                                     ids.numel(), scale, out.data_ptr(), _pitch(out, dim), sh),
-               "dfw_embed_lanes")
+    out = _embed_out(ids, dim, out, dev)
+    scope = LanesScope(dl.stream.data_ptr(), dl.mant.data_ptr(), dl.lut.data_ptr(), dl.chunk_bits.data_ptr(),
+                       dl.group_start.data_ptr(), ctypes.pointer(dl.table), ctypes.pointer(dl.info))
+    _check(lib().dfw_embed_lanes(ctypes.byref(scope), first, rows, dim, ids.data_ptr(), ids.dtype is torch.int64, ids.numel(),
+                                 scale, out.data_ptr(), _pitch(out, dim), sh), "dfw_embed_lanes")
     return out
 
 
@@ -707,13 +720,15 @@ def embed_rows(table: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, out: 
     """Rows of a bf16 embedding table [rows, dim] (a decoded scope's view) by
     token id, scaled (``dfw_embed_rows``); ids and result as :func:`embed_lanes`."""
     dev = table.device
+    sh = _here(dev, stream) if table.is_cuda else 0
+    if sh is None:
+        with _there(dev, stream):
+            return embed_rows(table, ids, scale, out)
     _expect("table", table, dev, _BF16, 2)
     rows, dim = table.shape
-    with _On(dev, stream) as sh:
-        out = _embed_out(ids, dim, out, dev)
-        _check(lib().dfw_embed_rows(table.data_ptr(), rows, dim, table.stride(0), ids.data_ptr(), ids.dtype == torch.int64,
-                                    ids.numel(), scale, out.data_ptr(), _pitch(out, dim), sh),
-               "dfw_embed_rows")
+    out = _embed_out(ids, dim, out, dev)
+    _check(lib().dfw_embed_rows(table.data_ptr(), rows, dim, table.stride(0), ids.data_ptr(), ids.dtype is torch.int64,
+                                ids.numel(), scale, out.data_ptr(), _pitch(out, dim), sh), "dfw_embed_rows")
     return out
 
 
@@ -731,27 +746,30 @@ def embed_grad(ids: torch.Tensor, dy: torch.Tensor, rows: int, scale: float = 1.
     _expect("ids", ids, dev, _IDS)
     if len(shape) == 0 or shape[:-1] != ids.shape or not ids.is_contiguous() or not _rows_contiguous(dy):
         raise ValueError("dy must have one contiguous row per id, ids must be contiguous")
+    sh = _here(dev, stream)
+    if sh is None:
+        with _there(dev, stream):
+            return embed_grad(ids, dy, rows, scale, out, out_dtype, accumulate, scratch)
     tokens, dim = ids.numel(), shape[-1]
-    with _On(dev, stream) as sh:
-        if out is None:
-            if accumulate:
-                raise ValueError("accumulate needs an out tensor")
-            if out_dtype not in _FLOATS:
-                raise TypeError(f"out_dtype {out_dtype}, expected one of {_FLOATS}")
-            out = torch.empty((rows, dim), dtype=out_dtype, device=dev)
-        else:
-            _expect("out", out, dev, _FLOATS)
-            if out.shape != (rows, dim) or not out.is_contiguous():
-                raise ValueError(f"out must be a contiguous [{rows}, {dim}] tensor")
-        if scratch is None:
-            need = embed_grad_scratch_bytes(tokens, dim)
-            scratch = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-        else:
-            _expect("scratch", scratch, dev, _BYTES, 1)
-        _check(lib().dfw_embed_grad(ids.data_ptr(), ids.dtype == torch.int64, tokens, dy.data_ptr(), dy.dtype == torch.float32,
-                                    _pitch(dy, dim), rows, dim, scale, out.data_ptr(),
-                                    out.dtype == torch.float32, accumulate, None if scratch is None else scratch.data_ptr(),
-                                    0 if scratch is None else scratch.numel(), sh), "dfw_embed_grad")
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs an out tensor")
+        if out_dtype not in _FLOATS:
+            raise TypeError(f"out_dtype {out_dtype}, expected one of {_FLOATS}")
+        out = dy.new_empty((rows, dim), dtype=out_dtype)
+    else:
+        _expect("out", out, dev, _FLOATS)
+        if out.shape != (rows, dim) or not out.is_contiguous():
+            raise ValueError(f"out must be a contiguous [{rows}, {dim}] tensor")
+    if scratch is None:
+        need = embed_grad_scratch_bytes(tokens, dim)
+        scratch = dy.new_empty((need,), dtype=torch.uint8) if need else None
+    else:
+        _expect("scratch", scratch, dev, _BYTES, 1)
+    _check(lib().dfw_embed_grad(ids.data_ptr(), ids.dtype is torch.int64, tokens, dy.data_ptr(), dy.dtype is torch.float32,
+                                _pitch(dy, dim), rows, dim, scale, out.data_ptr(), out.dtype is torch.float32, accumulate,
+                                None if scratch is None else scratch.data_ptr(), 0 if scratch is None else scratch.numel(), sh),
+           "dfw_embed_grad")
     return out
 
 
