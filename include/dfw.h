@@ -728,8 +728,9 @@ dfw_status dfw_q4_dequantise(const uint8_t *d_packed, const dfw_q4_info *info, u
  * Arithmetic: (q - z) and x are exact in bf16 and their products exact; a
  * group's products are summed in fp32, the sums multiplied by their scales
  * and added in fp32, in an order fixed by the shape (repeated calls give
- * identical bits); a bf16 result is rounded once.  Asynchronous; needs no
- * scratch.  Errors: DFW_EINVAL, DFW_EALIGN (d_packed 16 bytes, d_x and d_y
+ * identical bits); a bf16 result is rounded once.  More than 16 vectors (8 or
+ * 4 for more than 24576 or 32768 columns) read the weights again for every 16.
+ * d_y must not overlap an input.  Asynchronous; needs no scratch.  Errors: DFW_EINVAL, DFW_EALIGN (d_packed 16 bytes, d_x and d_y
  * their element), DFW_ECUDA.
  */
 dfw_status dfw_q4_gemv(const uint8_t *d_packed, const dfw_q4_info *info, uint32_t m, const uint16_t *d_x,
@@ -753,8 +754,8 @@ dfw_status dfw_q4_gemv(const uint8_t *d_packed, const dfw_q4_info *info, uint32_
  *   d_out    device, bf16, row t at d_out + t ld_out (ld_out >= dim)
  * dfw_embed_rows -- the table is bf16 (a decoded scope): row v at
  * d_table + v ld_table (ld_table >= dim).
- * Limits: tokens <= DFW_EMBED_MAX_TOKENS, rows <= DFW_EMBED_MAX_ROWS, dim <=
- * DFW_EMBED_MAX_DIM.  Errors: DFW_EINVAL, DFW_EALIGN (ids and bf16 pointers
+ * d_out must not overlap an input.  Limits: tokens <= DFW_EMBED_MAX_TOKENS,
+ * rows <= DFW_EMBED_MAX_ROWS, dim <= DFW_EMBED_MAX_DIM.  Errors: DFW_EINVAL, DFW_EALIGN (ids and bf16 pointers
  * to their element, the scope's buffers as dfw_decode_lanes), DFW_ECUDA.
  */
 #define DFW_EMBED_MAX_TOKENS 1048576u

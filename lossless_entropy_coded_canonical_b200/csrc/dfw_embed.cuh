@@ -375,6 +375,16 @@ __global__ void __launch_bounds__(256) embed_single_rows(const RowsOfLanes p) {
 
 // ------------------------------------------------------ the table's gradient
 
+// Thread `me` of `all` zeroes its share of n bytes.
+__device__ __forceinline__ void zero_span(uint8_t *p, uint64_t n, uint64_t me, uint64_t all) {
+    const uint64_t head = min(n, (uint64_t)(-reinterpret_cast<uintptr_t>(p) & 31u));
+    const uint64_t body = (n - head) >> 5, tail = n - head - (body << 5);
+    if (me < head) p[me] = 0;
+    if (me < tail) p[n - 1u - me] = 0;
+    const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+    for (uint64_t i = me; i < body; i += all) stg256_cs(p + head + (i << 5), z, z);
+}
+
 // Sorting.  A cluster of C CTAs sorts a block of up to 1024 C IPT tokens by
 // row, stably: up to 8 bits a pass from the lowest.  Each warp ranks its own run of
 // tokens (equal digits of 32 tokens found by a ballot per bit: no atomics, a
@@ -392,6 +402,9 @@ struct SortParams {
     uint32_t *keys, *pos;  // per block: sorted keys and the tokens they belong to
     uint32_t *joins;       // the two counters of JoinLists, cleared here
     uint32_t passes, bits;  // digits of a key and their width, at most 8
+    uint32_t ctas;         // CTAs that sort; those past them zero the gradient
+    uint8_t *fill;
+    uint64_t fill_bytes;
 };
 
 template <int C, int IPT, bool PACK>
@@ -413,6 +426,11 @@ __global__ void __launch_bounds__(SORT_THREADS, 1) grad_sort(const SortParams p)
     const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
     const uint32_t rank = blockIdx.x % C, base = blockIdx.x * CAP, run = warp * 32u * IPT + lane;
     griddep_launch_dependents();
+    if (blockIdx.x >= p.ctas) {  // (whole clusters)
+        zero_span(p.fill, p.fill_bytes, (uint64_t)(blockIdx.x - p.ctas) * SORT_THREADS + tid,
+                  (uint64_t)(gridDim.x - p.ctas) * SORT_THREADS);
+        return;
+    }
     if (blockIdx.x == 0u && tid < 2u) p.joins[tid] = 0u;
     const uint32_t block = base - rank * CAP;  // the cluster's first token
     uint32_t key[IPT], pos[PACK ? 1 : IPT];  // PACK: key[j] holds both
@@ -539,19 +557,13 @@ __global__ void __launch_bounds__(SORT_THREADS, 1) grad_sort(const SortParams p)
     }
 }
 
-// Thread `me` of `all` zeroes its share of n bytes.
-__device__ __forceinline__ void zero_span(uint8_t *p, uint64_t n, uint64_t me, uint64_t all) {
-    const uint64_t head = min(n, (uint64_t)(-reinterpret_cast<uintptr_t>(p) & 31u));
-    const uint64_t body = (n - head) >> 5, tail = n - head - (body << 5);
-    if (me < head) p[me] = 0;
-    if (me < tail) p[n - 1u - me] = 0;
-    const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-    for (uint64_t i = me; i < body; i += all) stg256_cs(p + head + (i << 5), z, z);
-}
+// Zeroes a large gradient while the tokens are sorted: a programmatic
+// dependent of the sort that starts beside it, and ends after it (so that what
+// follows on the stream follows both).  A small one (FILL_BESIDE) is zeroed by
+// CTAs of the sort's own launch; more of those would wait for each other, as a
+// cluster's CTAs find fewer SMs (262 MB beside 8192 tokens: 55 us, 42 here).
+constexpr uint64_t FILL_BESIDE = 4u << 20;
 
-// Zeroes the gradient while the tokens are sorted: a programmatic dependent
-// of the sort that starts beside it, and ends after it (so that what follows
-// on the stream follows both).
 __global__ void __launch_bounds__(512) grad_zero(uint8_t *p, uint64_t n) {
     griddep_launch_dependents();
     zero_span(p, n, (uint64_t)blockIdx.x * blockDim.x + threadIdx.x, (uint64_t)gridDim.x * blockDim.x);
@@ -1071,7 +1083,7 @@ uint64_t embed_grad_scratch(uint64_t tokens, uint32_t dim) {
 }
 
 template <int C, int IPT, bool PACK>
-dfw_status launch_grad_sort(const SortParams &p, uint32_t blocks, cudaStream_t s) {
+dfw_status launch_grad_sort(SortParams p, uint32_t blocks, cudaStream_t s) {
     static int opted[16];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 16) return DFW_ECUDA;
@@ -1081,7 +1093,9 @@ dfw_status launch_grad_sort(const SortParams &p, uint32_t blocks, cudaStream_t s
             return DFW_ECUDA;
         opted[dev] = 1;
     }
-    return launch_with(grad_sort<C, IPT, PACK>, blocks * C, SORT_THREADS, smem, false, C, s, p);
+    p.ctas = blocks * C;
+    const uint64_t fillers = (p.fill_bytes + (1u << 16) - 1u) >> 16;  // 64 KB each, in whole clusters
+    return launch_with(grad_sort<C, IPT, PACK>, p.ctas + (fillers + C - 1u) / C * C, SORT_THREADS, smem, false, C, s, p);
 }
 template <bool PACK>
 dfw_status launch_grad_sort(const SortParams &p, const GradCut &cut, cudaStream_t s) {
@@ -1161,9 +1175,11 @@ dfw_status launch_embed_grad(const void *d_ids, int ids64, uint64_t tokens, cons
     while (rows >> key_bits) ++key_bits;  // keys go up to `rows`
     sp.passes = (key_bits + 7u) / 8u;
     sp.bits = (key_bits + sp.passes - 1u) / sp.passes;
+    sp.fill = fill;
+    sp.fill_bytes = fill_bytes <= FILL_BESIDE ? fill_bytes : 0u;
     st = key_bits <= 16u ? launch_grad_sort<true>(sp, cut, s) : launch_grad_sort<false>(sp, cut, s);
     if (st != DFW_OK) return st;
-    if (fill_bytes && (st = launch_with(grad_zero, fillers, 512, 0, true, 1, s, fill, fill_bytes)) != DFW_OK) return st;
+    if (fill_bytes > FILL_BESIDE && (st = launch_with(grad_zero, fillers, 512, 0, true, 1, s, fill, fill_bytes)) != DFW_OK) return st;
     ReduceParams p;
     p.keys = lists[0];
     p.pos = lists[1];

@@ -250,10 +250,20 @@ __global__ void __launch_bounds__(256) q4_dequantise_tiles(const uint8_t *__rest
 // warps' order.  When the vectors are too long for one SM's shared memory, a
 // cluster of 2 to 8 CTAs shares the columns and joins its sums the same way.
 // Up to 8 vectors take 32 warps of 64 registers, or 16 where their shared
-// memory does not allow 32; 9 to 16 have twice the sums and take 16.
+// memory does not allow 32 or the CTA has few tiles; 9 to 16 have twice the
+// sums and take 16.
+//
+// What bounds it: 128256 x 4096 with 4 vectors takes 54.5 us, 5.0 TB/s of the
+// 6.5 a copy reaches.  The same loop runs in 43.5 us (6.3 TB/s) with neither
+// expansion nor products, in 45.8 with the products alone, in 48.7 with the
+// expansion alone: the two do not overlap fully, at 142 warp instructions per
+// tile and 65% of the issue slots; no single pipe is above half its rate, and
+// data already in L2 run no faster.  Small matrices are bound by the chain of
+// a launch, the first copies, and the join: 1024 x 4096, one vector, 3.8 us.
 constexpr uint32_t Q4_STEP = 2;                   // tiles a warp takes at a time
 constexpr uint32_t Q4_JOIN_BYTES = 16u * 1024u;   // a CTA's buffer for its cluster's sums
-__host__ __device__ constexpr uint32_t q4_ring(int nt, uint32_t warps) { return nt == 1 && warps == 16u ? 3u : 2u; }  // steps in a warp's ring
+// Steps in a warp's ring: three where 16 warps leave room for them.
+__host__ __device__ constexpr uint32_t q4_ring(int nt, uint32_t warps) { return nt == 1 && warps == 16u ? 3u : 2u; }
 
 struct Q4GemvParams {
     Q4Params q;
@@ -308,7 +318,7 @@ __device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t 
 // in the halves of e[i].  off: -z / 64 in both halves.
 __device__ __forceinline__ void q4_expand(uint32_t word, uint32_t off, uint32_t (&e)[4]) {
     constexpr uint32_t LOW = 0x7F007F00u, HIGH = 0x7D007D00u;  // 2^127, 2^123
-    const uint32_t up = __umulhi(word, 1u << 24);              // word >> 8, on the multiply-add pipe
+    const uint32_t up = word >> 8;
     e[0] = fma_bf16x2(word & 0x000F000Fu, LOW, off);
     e[1] = fma_bf16x2(word & 0x00F000F0u, HIGH, off);
     e[2] = fma_bf16x2(up & 0x000F000Fu, LOW, off);
@@ -432,7 +442,8 @@ __global__ void __launch_bounds__(32 * W, 1) q4_gemv_tiles(const Q4GemvParams a)
         if (in_left >= Q4_STEP && (!SPLIT || in_ct + Q4_STEP <= cts)) {  // a whole step, contiguous
 #pragma unroll
             for (uint32_t at = 0; at < SLOT; at += 512u)
-                if ((at + 512u <= SLOT || lane < (SLOT - at) / 16u) && in_bounds(slot_in + at, src + at)) cp_async16(slot_in + at, src + at);
+                if ((at + 512u <= SLOT || lane < (SLOT - at) / 16u) && in_bounds(slot_in + at, src + at))
+                    cp_async16(slot_in + at, src + at);
             src += SLOT;
             in_left -= Q4_STEP;
             in_ct += Q4_STEP;
@@ -445,7 +456,8 @@ __global__ void __launch_bounds__(32 * W, 1) q4_gemv_tiles(const Q4GemvParams a)
                 const uint32_t dst = slot_in + u * TILE;
                 if (in_bounds(dst, src)) cp_async16(dst, src);
                 if (in_bounds(dst + 512u, src + 512)) cp_async16(dst + 512u, src + 512);
-                if (lane < (TILE - Q4_CODES) / 16u && in_bounds(dst + Q4_CODES, src + Q4_CODES)) cp_async16(dst + Q4_CODES, src + Q4_CODES);
+                if (lane < (TILE - Q4_CODES) / 16u && in_bounds(dst + Q4_CODES, src + Q4_CODES))
+                    cp_async16(dst + Q4_CODES, src + Q4_CODES);
                 src += TILE;
                 if (SPLIT && ++in_ct == cts) {
                     in_ct = 0;
@@ -512,7 +524,8 @@ __global__ void __launch_bounds__(32 * W, 1) q4_gemv_tiles(const Q4GemvParams a)
 #pragma unroll
             for (uint32_t u = 0; u < Q4_STEP; ++u) {
                 if (i + u >= hi) break;
-                q4_tile_products<GT, Z, NT>(Q4Tile<GT, Z>(slot + u * TILE, slot + u * TILE - 16u * lane + 2u * GT * g, g), x0 + 256u * ct, nt_step, acc);
+                const uint32_t cp = slot + u * TILE, sp = cp - 16u * lane + 2u * GT * g;
+                q4_tile_products<GT, Z, NT>(Q4Tile<GT, Z>(cp, sp, g), x0 + 256u * ct, nt_step, acc);
                 if (++ct == cts) {
                     put_away(row++);
                     ct = 0;
@@ -532,8 +545,12 @@ __global__ void __launch_bounds__(32 * W, 1) q4_gemv_tiles(const Q4GemvParams a)
 #pragma unroll 8
                 for (uint32_t w = w0; w < w1; ++w) v += sums[(w + r) * outs + o];
             }
-            if constexpr (!SPLIT) q4_store(a, (uint64_t)Q4_ROWS * (rt0 + done + r) + (o & 15u), o >> 4, v);
-            else if (check((((r / split) * split + rank) * outs + o) * 4u < Q4_JOIN_BYTES, CK_Q4_SUMS)) st_cluster_f32(map_rank(smem_u32(join + ((r / split) * split + rank) * outs + o), r % split), v);
+            if constexpr (!SPLIT) {
+                q4_store(a, (uint64_t)Q4_ROWS * (rt0 + done + r) + (o & 15u), o >> 4, v);
+            } else {
+                const uint32_t at = (r / split * split + rank) * outs + o;
+                if (check(at * 4u < Q4_JOIN_BYTES, CK_Q4_SUMS)) st_cluster_f32(map_rank(smem_u32(join + at), r % split), v);
+            }
         }
         if constexpr (SPLIT) {  // row tile r of the pass is added up by CTA r mod split
             cluster_sync();
