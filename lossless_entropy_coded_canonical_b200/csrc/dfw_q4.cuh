@@ -277,6 +277,8 @@ struct Q4GemvParams {
     uint32_t pitch;    // bytes from one vector to the next in shared memory
     uint32_t pass;     // row tiles between two joins of the warps' sums
     uint32_t share, extra;  // row tiles per cluster, and how many clusters take one more
+    uint32_t outs_inv; // ceil(2^32 / (16 m)): i / (16 m) is the high word of i times it (i below 2^24)
+    uint32_t threads_log;  // log2 of the threads that copy a vector
     uint32_t xvec;     // the vectors can be read 16 bytes at a time
 };
 
@@ -472,19 +474,20 @@ __global__ void __launch_bounds__(32 * W, 1) q4_gemv_tiles(const Q4GemvParams a)
 #pragma unroll
     for (uint32_t u = 0; u + 1u < RING; ++u) fetch();
 
-    // the vectors' columns [128 ct0, 128 (ct0 + cts)), zeros past the matrix
-    for (uint32_t v = 0; v < a.m; ++v) {
-        for (uint32_t c = threadIdx.x; c < 16u * cts; c += 32u * W) {
-            const uint32_t col = Q4_COLS * ct0 + 8u * c;
-            const uint16_t *x = a.x + v * a.ldx + col;
-            uint8_t *dst = vecs + v * a.pitch + 16u * c;
-            if (col >= a.q.cols) {
-                *reinterpret_cast<uint4 *>(dst) = make_uint4(0u, 0u, 0u, 0u);
+    // the vectors' columns [128 ct0, 128 (ct0 + cts)), zeros past the matrix; 2^log threads to a vector
+    const uint32_t log = a.threads_log, v = threadIdx.x >> log;
+    if (v < a.m) {
+        const uint16_t *x = a.x + v * a.ldx + Q4_COLS * ct0;
+        uint8_t *dst = vecs + v * a.pitch;
+        const uint32_t here = (min(a.q.cols, Q4_COLS * (ct0 + cts)) - min(a.q.cols, Q4_COLS * ct0)) / 8u;
+        for (uint32_t c = threadIdx.x & ((1u << log) - 1u); c < 16u * cts; c += 1u << log) {
+            if (c >= here) {
+                *reinterpret_cast<uint4 *>(dst + 16u * c) = make_uint4(0u, 0u, 0u, 0u);
             } else if (a.xvec) {
-                cp_async16(smem_u32(dst), x);
+                cp_async16(smem_u32(dst + 16u * c), x + 8u * c);
             } else {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) reinterpret_cast<uint16_t *>(dst)[j] = __ldg(x + j);
+                for (int j = 0; j < 8; ++j) reinterpret_cast<uint16_t *>(dst + 16u * c)[j] = __ldg(x + 8u * c + j);
             }
         }
     }
@@ -535,13 +538,18 @@ __global__ void __launch_bounds__(32 * W, 1) q4_gemv_tiles(const Q4GemvParams a)
         }
         if (ct || lo == hi) put_away(row);  // (a warp without tiles puts zeros between its neighbours' sums)
         __syncthreads();
+        // row tile r's sums: those of the warps whose runs meet tiles [r cts,
+        // (r + 1) cts), from the first that ends behind r cts
+        const uint32_t tiles = n * cts, inv = cts ? 0xFFFFFFFFu / tiles : 0u;
+        auto quotient = [&](uint32_t x) {  // x / tiles (x below 2^25: the estimate is at most one short)
+            const uint32_t q = __umulhi(x, inv);
+            return (q + 1u) * tiles <= x ? q + 1u : q;
+        };
         for (uint32_t i = threadIdx.x; i < n * outs; i += 32u * W) {
-            const uint32_t r = i / outs, o = i - r * outs;
-            // the warps whose runs meet tiles [r cts, (r + 1) cts): from the first that ends behind r cts
+            const uint32_t r = __umulhi(i, a.outs_inv), o = i - r * outs;
             float v = 0.f;
             if (cts) {
-                const uint32_t tiles = n * cts, w0 = ((r * cts + 1u) * W + tiles - 1u) / tiles - 1u;
-                const uint32_t w1 = ((r + 1u) * cts * W + tiles - 1u) / tiles;
+                const uint32_t w0 = quotient((r * cts + 1u) * W + tiles - 1u) - 1u, w1 = quotient((r + 1u) * cts * W + tiles - 1u);
 #pragma unroll 8
                 for (uint32_t w = w0; w < w1; ++w) v += sums[(w + r) * outs + o];
             }
@@ -554,8 +562,9 @@ __global__ void __launch_bounds__(32 * W, 1) q4_gemv_tiles(const Q4GemvParams a)
         }
         if constexpr (SPLIT) {  // row tile r of the pass is added up by CTA r mod split
             cluster_sync();
-            for (uint32_t i = threadIdx.x; rank + i / outs * split < n; i += 32u * W) {
-                const uint32_t r = rank + i / outs * split, o = i % outs;
+            for (uint32_t i = threadIdx.x;; i += 32u * W) {
+                const uint32_t mine = __umulhi(i, a.outs_inv), r = rank + mine * split, o = i - mine * outs;
+                if (r >= n) break;
                 const float *p = join + (r / split) * split * outs + o;
                 float v = p[0];
                 for (uint32_t w = 1; w < split; ++w) v += p[w * outs];
@@ -715,6 +724,9 @@ dfw_status launch_q4_pass(Q4GemvParams a, int dev, int sms, cudaStream_t s) {
     uint64_t room = 1u + (SMEM_MOST - smem) / (64u * a.m);
     if (split > 1u) room = std::min<uint64_t>(room, Q4_JOIN_BYTES / (64u * a.m) / split * split);
     a.pass = (uint32_t)std::min(rows, room);
+    a.outs_inv = (uint32_t)(((1ull << 32) + 16u * a.m - 1u) / (16u * a.m));
+    a.threads_log = warps == 32u ? 10u : 9u;
+    for (uint32_t k = 1; k < a.m; k *= 2u) --a.threads_log;
     a.share = (uint32_t)(a.q.row_tiles / clusters);
     a.extra = (uint32_t)(a.q.row_tiles % clusters);
     smem += (a.pass - 1u) * 64u * a.m;
