@@ -253,13 +253,13 @@ __global__ void __launch_bounds__(256) q4_dequantise_tiles(const uint8_t *__rest
 // memory does not allow 32 or the CTA has few tiles; 9 to 16 have twice the
 // sums and take 16.
 //
-// What bounds it: 128256 x 4096 with 4 vectors takes 54.5 us, 5.0 TB/s of the
-// 6.5 a copy reaches.  The same loop runs in 43.5 us (6.3 TB/s) with neither
-// expansion nor products, in 45.8 with the products alone, in 48.7 with the
-// expansion alone: the two do not overlap fully, at 142 warp instructions per
-// tile and 65% of the issue slots; no single pipe is above half its rate, and
-// data already in L2 run no faster.  Small matrices are bound by the chain of
-// a launch, the first copies, and the join: 1024 x 4096, one vector, 3.8 us.
+// What bounds it: 128256 x 4096 with 4 vectors takes 48.8 us, 5.6 TB/s of the
+// 6.5 a copy reaches; the same loop takes 46.1 us with neither expansion nor
+// products, so the copies bound it (the shift in the expansion as a
+// multiplication's high half, meant to spare the integer pipe, made that
+// 54.5).  Small matrices are bound by the chain of a launch, the first copies
+// and the join: 1024 x 4096, one vector, 3.7 us, of which a launch of one tile
+// takes 2.7; 6144 x 4096 7.2 us, 6.2 without the arithmetic.
 constexpr uint32_t Q4_STEP = 2;                   // tiles a warp takes at a time
 constexpr uint32_t Q4_JOIN_BYTES = 16u * 1024u;   // a CTA's buffer for its cluster's sums
 // Steps in a warp's ring: three where 16 warps leave room for them.
