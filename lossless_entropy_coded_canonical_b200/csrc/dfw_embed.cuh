@@ -14,6 +14,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <cstring>
 
 #include "dfw_lanes.cuh"
 #include "dfw_q4.cuh"
@@ -42,21 +43,41 @@ __device__ __forceinline__ bool token_row(const IdSource &s, uint32_t t, uint64_
     return true;
 }
 
-// Two bf16(scale w), each rounded to nearest even; scale 1 keeps the bits
-// (NaN payloads included), as the decoder does.  (One packed bf16
-// multiplication where the scale is a bf16 itself measured 1-3% slower: the
-// choice costs more than the arithmetic it saves.)
-__device__ __forceinline__ uint32_t scaled2(uint32_t w, float scale, bool one) {
-    if (one) return w;
-    const float lo = __uint_as_float(w << 16) * scale, hi = __uint_as_float(w & 0xFFFF0000u) * scale;
+// bf16(scale w), rounded to nearest even, of two weights at a time.  Scale 1
+// keeps the bits (NaN payloads included), as the decoder does.  A scale that is
+// a bf16 itself takes one packed multiplication: the 16-bit products are exact
+// before its one rounding, so the result is the fp32 product's, rounded.
+enum ScaleKind { SCALE_ONE, SCALE_BF16, SCALE_FP32 };
+struct RowScale {
+    float f;
+    uint32_t pair;  // the scale's upper half, twice
+    ScaleKind kind;
+};
+RowScale row_scale(float scale) {
+    uint32_t u;
+    std::memcpy(&u, &scale, 4);
+    return {scale, (u >> 16) * 0x10001u, scale == 1.f ? SCALE_ONE : (u & 0xFFFFu) == 0u ? SCALE_BF16 : SCALE_FP32};
+}
+template <ScaleKind KIND>
+__device__ __forceinline__ uint32_t scaled2(uint32_t w, const RowScale &s) {
+    if constexpr (KIND == SCALE_ONE) return w;
     uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    if constexpr (KIND == SCALE_BF16) {
+        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(w), "r"(s.pair));
+    } else {
+        const float lo = __uint_as_float(w << 16) * s.f, hi = __uint_as_float(w & 0xFFFF0000u) * s.f;
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    }
     return r;
 }
-__device__ __forceinline__ uint4 scaled8(uint4 w, float scale, bool one) {
-    return make_uint4(scaled2(w.x, scale, one), scaled2(w.y, scale, one), scaled2(w.z, scale, one), scaled2(w.w, scale, one));
+template <ScaleKind KIND>
+__device__ __forceinline__ uint4 scaled8(uint4 w, const RowScale &s) {
+    return make_uint4(scaled2<KIND>(w.x, s), scaled2<KIND>(w.y, s), scaled2<KIND>(w.z, s), scaled2<KIND>(w.w, s));
 }
-__device__ __forceinline__ uint16_t scaled1(uint32_t w, float scale, bool one) { return (uint16_t)scaled2(w, scale, one); }
+template <ScaleKind KIND>
+__device__ __forceinline__ uint16_t scaled1(uint32_t w, const RowScale &s) {
+    return (uint16_t)scaled2<KIND>(w, s);
+}
 
 // ------------------------------------------------------- rows of a bf16 table
 
@@ -66,25 +87,16 @@ struct RowsOfTable {
     uint16_t *out;
     uint64_t ldt, ldo;
     uint32_t dim, parts;  // parts: pieces of EMBED_PART a row is cut into
-    float scale;
+    RowScale scale;
 };
 
 // A warp copies one piece of a row: VEC weights per lane and access, four
 // accesses in flight.
 constexpr uint32_t EMBED_PART = 1024;
 
-template <int VEC>
-__global__ void __launch_bounds__(256) embed_table_rows(const RowsOfTable p) {
-    const bool one = p.scale == 1.f;
-    const uint32_t lane = threadIdx.x & 31u;
-    const uint64_t piece = blockIdx.x * 8ull + (threadIdx.x >> 5);
-    const uint32_t t = (uint32_t)(piece / p.parts), c0 = (uint32_t)(piece % p.parts) * EMBED_PART;
-    if (t >= p.ids.tokens) return;
-    uint64_t row = 0;
-    const bool have = token_row(p.ids, t, row, lane == 0u);
-    const uint16_t *src = p.table + row * p.ldt;
-    uint16_t *dst = p.out + t * p.ldo;
-    const uint32_t end = min(p.dim, c0 + EMBED_PART);
+template <ScaleKind KIND, int VEC>
+__device__ __forceinline__ void copy_piece(const RowScale &s, const uint16_t *src, uint16_t *dst, uint32_t c0, uint32_t end,
+                                           bool have, uint32_t lane) {
     if constexpr (VEC == 8) {
         uint4 v[4];
 #pragma unroll
@@ -96,11 +108,29 @@ __global__ void __launch_bounds__(256) embed_table_rows(const RowsOfTable p) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const uint32_t c = c0 + 256u * i + 8u * lane;
-            if (c < end) __stcs(reinterpret_cast<uint4 *>(dst + c), scaled8(v[i], p.scale, one));
+            if (c < end) __stcs(reinterpret_cast<uint4 *>(dst + c), have ? scaled8<KIND>(v[i], s) : v[i]);
         }
     } else {
 #pragma unroll 8
-        for (uint32_t c = c0 + lane; c < end; c += 32u) dst[c] = have ? scaled1(__ldg(src + c), p.scale, one) : (uint16_t)0;
+        for (uint32_t c = c0 + lane; c < end; c += 32u) dst[c] = have ? scaled1<KIND>(__ldg(src + c), s) : (uint16_t)0;
+    }
+}
+
+template <int VEC>
+__global__ void __launch_bounds__(256) embed_table_rows(const RowsOfTable p) {
+    const uint32_t lane = threadIdx.x & 31u;
+    const uint64_t piece = blockIdx.x * 8ull + (threadIdx.x >> 5);
+    const uint32_t t = (uint32_t)(piece / p.parts), c0 = (uint32_t)(piece % p.parts) * EMBED_PART;
+    if (t >= p.ids.tokens) return;
+    uint64_t row = 0;
+    const bool have = token_row(p.ids, t, row, lane == 0u);
+    const uint16_t *src = p.table + row * p.ldt;
+    uint16_t *dst = p.out + t * p.ldo;
+    const uint32_t end = min(p.dim, c0 + EMBED_PART);
+    switch (p.scale.kind) {
+        case SCALE_ONE: copy_piece<SCALE_ONE, VEC>(p.scale, src, dst, c0, end, have, lane); break;
+        case SCALE_BF16: copy_piece<SCALE_BF16, VEC>(p.scale, src, dst, c0, end, have, lane); break;
+        default: copy_piece<SCALE_FP32, VEC>(p.scale, src, dst, c0, end, have, lane);
     }
 }
 
@@ -116,12 +146,48 @@ struct RowsOfLanes {
     uint32_t dim;
     uint32_t units;        // units a token's row is cut into: its groups if rows are whole groups or parts of one, else 1
     uint32_t single;       // total_bits == 0: every exponent is this one
-    float scale;
+    RowScale scale;
 };
 
 // Writes zeros to weights [c0, c1) of a token's row.
 __device__ __forceinline__ void zero_row(uint16_t *out, uint32_t c0, uint32_t c1, uint32_t lane) {
     for (uint32_t c = c0 + lane; c < c1; c += 32u) out[c] = 0;
+}
+
+// Joins, scales and writes weights [lo, hi) of a decoded group (raw bytes at
+// mbuf, exponents at exps0) to out + lo, out + lo + 1, ...
+template <ScaleKind KIND, int V>
+__device__ __forceinline__ void join_row(const RowScale &s, uint16_t *out, uint32_t lo, uint32_t hi, uint32_t mbuf,
+                                         uint32_t exps0, uint32_t lane) {
+    if constexpr (V == 16) {
+        const uint32_t mrow = mbuf + 16u * lane, erow = exps0 + 4u * (lane >> 2) + 4u * EXP_STRIDE * (lane & 3u);
+#pragma unroll
+        for (uint32_t j = 0; j < 4u; ++j) {
+            const uint32_t i = 512u * j + 16u * lane;
+            if (i < lo || i >= hi || !check(i + V <= hi, CK_EMBED_STORE)) continue;
+            uint4 a, b;
+            join16(mrow + 512u * j, erow + 32u * j, a, b);
+            stg256_cs(out + i, scaled8<KIND>(a, s), scaled8<KIND>(b, s));
+        }
+    } else if constexpr (V == 8) {
+#pragma unroll
+        for (uint32_t j = 0; j < 8u; ++j) {  // piece lane + 32 j: words 2 (piece mod 8) and + 1 of chunk piece / 8
+            const uint32_t piece = lane + 32u * j, i = 8u * piece;
+            if (i < lo || i >= hi || !check(i + V <= hi, CK_EMBED_STORE)) continue;
+            const uint32_t e = exps0 + 4u * (piece >> 3) + 2u * EXP_STRIDE * (piece & 7u), m = mbuf + 8u * piece;
+            uint4 v;
+            join4(lds32(e), lds32(m), v.x, v.y);
+            join4(lds32(e + EXP_STRIDE), lds32(m + 4u), v.z, v.w);
+            __stcs(reinterpret_cast<uint4 *>(out + i), scaled8<KIND>(v, s));
+        }
+    } else {
+#pragma unroll 4
+        for (uint32_t i = lo + lane; i < hi; i += 32u) {
+            const uint32_t e = lds32(exps0 + 4u * (i >> 6) + EXP_STRIDE * ((i & 63u) >> 2)) >> (8u * (i & 3u));
+            const uint32_t m = lds32(mbuf + (i & ~3u)) >> (8u * (i & 3u));
+            out[i] = scaled1<KIND>(join1(e & 0xFFu, m & 0xFFu), s);
+        }
+    }
 }
 
 // The decode kernel's work on chosen groups: a warp takes the groups of a
@@ -151,8 +217,6 @@ __global__ void __launch_bounds__(NT) embed_lanes_rows(const RowsOfLanes p) {
     const uint32_t exps0 = smem_u32(mbuf + GROUP_SYMS), exps = exps0 + 4u * lane;
     const uint32_t *g_hier = prm.lut + 2u * n_fast;
     const uint32_t kshift = 32u - prm.fast_bits;
-    const bool one = p.scale == 1.f;
-
     if (lane == 0u) {
         mbar_init(bar_s0, 1);
         mbar_init(bar_s0 + 8u, 1);
@@ -171,30 +235,38 @@ __global__ void __launch_bounds__(NT) embed_lanes_rows(const RowsOfLanes p) {
         uint64_t s0, s1;      // the group's bits
         uint32_t t, g, last;  // token, group, the unit's last group
     };
-    const uint32_t n_units = p.ids.tokens * p.units, stride = gridDim.x * NWARP;
-    uint32_t unit = warp * gridDim.x + blockIdx.x;
+    // this warp's units: token `at_t`, part `part` of its row, then every
+    // `stride` units further (t_step tokens and p_step parts)
+    const uint32_t stride = gridDim.x * NWARP, t_step = stride / p.units, p_step = stride % p.units;
+    const uint32_t unit0 = warp * gridDim.x + blockIdx.x;
+    uint32_t at_t = unit0 / p.units, part = unit0 % p.units;
     uint64_t row_ahead = 0;
-    bool have_ahead = unit < n_units && token_row(p.ids, unit / p.units, row_ahead, lane == 0u && unit % p.units == 0u);
+    bool have_ahead = at_t < p.ids.tokens && token_row(p.ids, at_t, row_ahead, lane == 0u && part == 0u);
     // the next group: the unit's next one, or the first of the next unit with a row
     auto advance = [&](Item &it, bool in_unit) {
         if (in_unit && it.g < it.last) {
             ++it.g;
         } else {
             for (;;) {
-                if (unit >= n_units) return false;
-                const uint32_t t = unit / p.units, part = unit % p.units;
+                if (at_t >= p.ids.tokens) return false;
+                const uint32_t t = at_t, at = part;
                 const bool have = have_ahead;
                 const uint64_t row = row_ahead;
-                unit += stride;
-                have_ahead = unit < n_units && token_row(p.ids, unit / p.units, row_ahead, lane == 0u && unit % p.units == 0u);
+                at_t += t_step;
+                part += p_step;
+                if (part >= p.units) {
+                    part -= p.units;
+                    ++at_t;
+                }
+                have_ahead = at_t < p.ids.tokens && token_row(p.ids, at_t, row_ahead, lane == 0u && part == 0u);
                 if (!have) {
-                    const uint32_t c0 = part * GROUP_SYMS;
-                    zero_row(p.out + t * p.ldo, c0, part + 1u < p.units ? c0 + GROUP_SYMS : p.dim, lane);
+                    const uint32_t c0 = at * GROUP_SYMS;
+                    zero_row(p.out + t * p.ldo, c0, at + 1u < p.units ? c0 + GROUP_SYMS : p.dim, lane);
                     continue;
                 }
                 it.t = t;
                 it.w0 = p.first + row * p.dim;
-                it.g = (uint32_t)(it.w0 / GROUP_SYMS) + part;
+                it.g = (uint32_t)(it.w0 / GROUP_SYMS) + at;
                 it.last = p.units > 1u ? it.g : (uint32_t)((it.w0 + p.dim - 1u) / GROUP_SYMS);
                 break;
             }
@@ -273,9 +345,11 @@ __global__ void __launch_bounds__(NT) embed_lanes_rows(const RowsOfLanes p) {
         const bool valid = __all_sync(0xFFFFFFFFu, cur.s1 - cur.s0 == gbits && cbits <= 32u * LANE_SYMS && span <= prm.sbuf_bytes &&
                                                        ((cur.s0 >> 3) & ~15ull) + span <= prm.stream_bytes &&
                                                        (n != 0u || cbits == 0u));
-        const uint64_t cw = (uint64_t)c * LANE_SYMS, end = cur.w0 + p.dim;
+        // the row's weights of the group: [lo, hi) of its 2048
+        const int64_t from = (int64_t)cur.w0 - (int64_t)cur.g * GROUP_SYMS;
+        const uint32_t lo = (uint32_t)max(from, (int64_t)0), hi = (uint32_t)min(from + p.dim, (int64_t)GROUP_SYMS);
         uint32_t err = 0;
-        if (ok && valid && cw < end && cw + n > cur.w0) {  // the row touches this chunk
+        if (ok && valid && LANE_SYMS * lane < hi && LANE_SYMS * lane + n > lo) {  // the row touches this chunk
             const uint32_t r = r0 + excl;
             uint32_t rd_end, wr_end;
             const uint32_t to = decode_chunk(smem_u32(slot + 64), r, (int)(8u * n), smem_u32(s_fast), kshift, g_hier,
@@ -303,37 +377,12 @@ __global__ void __launch_bounds__(NT) embed_lanes_rows(const RowsOfLanes p) {
             if (err) atomicOr(&g_status, err);
         } else {
             __syncwarp();  // the join reads other lanes' exponent slots
-            const uint64_t g0 = (uint64_t)cur.g * GROUP_SYMS;
-            uint16_t *out = p.out + cur.t * p.ldo;
-            if constexpr (V == 16) {
-                const uint32_t mrow = smem_u32(mbuf) + 16u * lane, erow = exps0 + 4u * (lane >> 2) + 4u * EXP_STRIDE * (lane & 3u);
-#pragma unroll
-                for (uint32_t j = 0; j < 4u; ++j) {
-                    const uint64_t w = g0 + 512u * j + 16u * lane;
-                    if (w < cur.w0 || w >= end || !check(w + V <= end, CK_EMBED_STORE)) continue;
-                    uint4 a, b;
-                    join16(mrow + 512u * j, erow + 32u * j, a, b);
-                    stg256_cs(out + (w - cur.w0), scaled8(a, p.scale, one), scaled8(b, p.scale, one));
-                }
-            } else if constexpr (V == 8) {
-#pragma unroll
-                for (uint32_t j = 0; j < 8u; ++j) {  // piece lane + 32 j: words 2 (piece mod 8) and + 1 of chunk piece / 8
-                    const uint32_t piece = lane + 32u * j;
-                    const uint64_t w = g0 + 8u * piece;
-                    if (w < cur.w0 || w >= end || !check(w + V <= end, CK_EMBED_STORE)) continue;
-                    const uint32_t e = exps0 + 4u * (piece >> 3) + 2u * EXP_STRIDE * (piece & 7u), m = smem_u32(mbuf) + 8u * piece;
-                    uint4 v;
-                    join4(lds32(e), lds32(m), v.x, v.y);
-                    join4(lds32(e + EXP_STRIDE), lds32(m + 4u), v.z, v.w);
-                    __stcs(reinterpret_cast<uint4 *>(out + (w - cur.w0)), scaled8(v, p.scale, one));
-                }
-            } else {
-                const uint32_t lo = (uint32_t)(max(cur.w0, g0) - g0), hi = (uint32_t)(min(end, g0 + GROUP_SYMS) - g0);
-#pragma unroll 4
-                for (uint32_t i = lo + lane; i < hi; i += 32u) {
-                    const uint32_t word = lds32(exps0 + 4u * (i >> 6) + EXP_STRIDE * ((i & 63u) >> 2));
-                    out[g0 + i - cur.w0] = scaled1(join1((word >> (8u * (i & 3u))) & 0xFFu, mbuf[i]), p.scale, one);
-                }
+            uint16_t *out = p.out + (int64_t)(cur.t * p.ldo) + ((int64_t)cur.g * GROUP_SYMS - (int64_t)cur.w0);
+            const uint32_t mb = smem_u32(mbuf);
+            switch (p.scale.kind) {
+                case SCALE_ONE: join_row<SCALE_ONE, V>(p.scale, out, lo, hi, mb, exps0, lane); break;
+                case SCALE_BF16: join_row<SCALE_BF16, V>(p.scale, out, lo, hi, mb, exps0, lane); break;
+                default: join_row<SCALE_FP32, V>(p.scale, out, lo, hi, mb, exps0, lane);
             }
         }
         if (!more) break;
@@ -346,9 +395,24 @@ __global__ void __launch_bounds__(NT) embed_lanes_rows(const RowsOfLanes p) {
 }
 
 // Rows of a scope with one exponent (no stream): raw bytes joined with it.
+template <ScaleKind KIND, int V>
+__device__ __forceinline__ void single_row(const RowScale &s, const uint8_t *m, uint32_t E, uint16_t *out, uint32_t dim, uint32_t lane) {
+#pragma unroll 4
+    for (uint32_t c = V * lane; c < dim; c += 32u * V) {
+        if constexpr (V == 8) {
+            const uint2 b = __ldg(reinterpret_cast<const uint2 *>(m + c));
+            uint4 v;
+            join4(E, b.x, v.x, v.y);
+            join4(E, b.y, v.z, v.w);
+            __stcs(reinterpret_cast<uint4 *>(out + c), scaled8<KIND>(v, s));
+        } else {
+            out[c] = scaled1<KIND>(join1(E & 0xFFu, __ldg(m + c)), s);
+        }
+    }
+}
+
 template <int V>
 __global__ void __launch_bounds__(256) embed_single_rows(const RowsOfLanes p) {
-    const bool one = p.scale == 1.f;
     const uint32_t E = rot_sym(p.single) * 0x01010101u, lane = threadIdx.x & 31u;
     for (uint32_t t = blockIdx.x * 8u + (threadIdx.x >> 5); t < p.ids.tokens; t += gridDim.x * 8u) {
         uint64_t row = 0;
@@ -358,17 +422,10 @@ __global__ void __launch_bounds__(256) embed_single_rows(const RowsOfLanes p) {
             continue;
         }
         const uint8_t *m = p.lanes.mant + p.first + row * p.dim;
-#pragma unroll 4
-        for (uint32_t c = V * lane; c < p.dim; c += 32u * V) {
-            if constexpr (V == 8) {
-                const uint2 b = __ldg(reinterpret_cast<const uint2 *>(m + c));
-                uint4 v;
-                join4(E, b.x, v.x, v.y);
-                join4(E, b.y, v.z, v.w);
-                __stcs(reinterpret_cast<uint4 *>(out + c), scaled8(v, p.scale, one));
-            } else {
-                out[c] = scaled1(join1(E & 0xFFu, __ldg(m + c)), p.scale, one);
-            }
+        switch (p.scale.kind) {
+            case SCALE_ONE: single_row<SCALE_ONE, V>(p.scale, m, E, out, p.dim, lane); break;
+            case SCALE_BF16: single_row<SCALE_BF16, V>(p.scale, m, E, out, p.dim, lane); break;
+            default: single_row<SCALE_FP32, V>(p.scale, m, E, out, p.dim, lane);
         }
     }
 }
@@ -966,7 +1023,7 @@ dfw_status launch_embed_rows(const uint16_t *d_table, uint64_t rows, uint32_t di
     p.ldt = ld_table;
     p.ldo = ld_out;
     p.dim = dim;
-    p.scale = scale;
+    p.scale = row_scale(scale);
     const bool vec = dim % 8u == 0u && ((reinterpret_cast<uintptr_t>(d_table) | reinterpret_cast<uintptr_t>(d_out)) & 15u) == 0u &&
                      (rows == 1u || ld_table % 8u == 0u) && (tokens == 1u || ld_out % 8u == 0u);
     p.parts = (dim + EMBED_PART - 1u) / EMBED_PART;
@@ -1029,7 +1086,7 @@ dfw_status launch_embed_lanes(const dfw_lanes_scope *scope, uint64_t first, uint
     p.ldo = ld_out;
     p.dim = dim;
     p.single = table->single_symbol;
-    p.scale = scale;
+    p.scale = row_scale(scale);
     const bool out16 = (reinterpret_cast<uintptr_t>(d_out) & 15u) == 0u && (tokens == 1u || ld_out % 8u == 0u);
     const bool out32 = (reinterpret_cast<uintptr_t>(d_out) & 31u) == 0u && (tokens == 1u || ld_out % 16u == 0u);
     if (table->total_bits == 0u) {
