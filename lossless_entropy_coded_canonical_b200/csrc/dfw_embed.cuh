@@ -118,6 +118,8 @@ __device__ __forceinline__ void copy_piece(const RowScale &s, const uint16_t *sr
 
 template <int VEC>
 __global__ void __launch_bounds__(256) embed_table_rows(const RowsOfTable p) {
+    griddep_wait();
+    griddep_launch_dependents();
     const uint32_t lane = threadIdx.x & 31u;
     const uint64_t piece = blockIdx.x * 8ull + (threadIdx.x >> 5);
     const uint32_t t = (uint32_t)(piece / p.parts), c0 = (uint32_t)(piece % p.parts) * EMBED_PART;
@@ -204,6 +206,8 @@ template <int NT, int V>
 __global__ void __launch_bounds__(NT) embed_lanes_rows(const RowsOfLanes p) {
     constexpr uint32_t NWARP = NT / 32;
     extern __shared__ __align__(16) uint8_t smem[];
+    griddep_wait();
+    griddep_launch_dependents();
     const LanesParams &prm = p.lanes;
     const uint32_t n_fast = 1u << prm.fast_bits;
     uint2 *s_fast = reinterpret_cast<uint2 *>(smem);
@@ -482,6 +486,7 @@ __global__ void __launch_bounds__(SORT_THREADS, 1) grad_sort(const SortParams p)
     uint32_t *l_key = C > 1 ? s_key + WORDS : s_key, *l_pos = l_key + CAP;  // this CTA's tokens in digit order
     const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
     const uint32_t rank = blockIdx.x % C, base = blockIdx.x * CAP, run = warp * 32u * IPT + lane;
+    griddep_wait();
     griddep_launch_dependents();
     if (blockIdx.x >= p.ctas) {  // (whole clusters)
         zero_span(p.fill, p.fill_bytes, (uint64_t)(blockIdx.x - p.ctas) * SORT_THREADS + tid,
@@ -926,6 +931,8 @@ template <typename DY, typename OUT, int VEC>
 __global__ void __launch_bounds__(256) grad_few(const FewParams p) {
     constexpr int U = 8;  // rows in flight
     __shared__ uint32_t s_row[GRAD_FEW], s_tok[GRAD_FEW], s_row2[GRAD_FEW], s_tok2[GRAD_FEW], s_count[GRAD_FEW / 32];
+    griddep_wait();
+    griddep_launch_dependents();
     const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
     const uint64_t r0 = (uint64_t)(blockIdx.x / p.col_blocks) * p.rows_per, r1 = min(r0 + p.rows_per, p.ids.rows);
     const uint32_t c0 = blockIdx.x % p.col_blocks * 256u * VEC, col = c0 + tid * VEC;
@@ -1027,7 +1034,7 @@ dfw_status launch_embed_rows(const uint16_t *d_table, uint64_t rows, uint32_t di
     const bool vec = dim % 8u == 0u && ((reinterpret_cast<uintptr_t>(d_table) | reinterpret_cast<uintptr_t>(d_out)) & 15u) == 0u &&
                      (rows == 1u || ld_table % 8u == 0u) && (tokens == 1u || ld_out % 8u == 0u);
     p.parts = (dim + EMBED_PART - 1u) / EMBED_PART;
-    return launch_with(vec ? embed_table_rows<8> : embed_table_rows<1>, (tokens * p.parts + 7u) / 8u, 256, 0, false, 1, s, p);
+    return launch_with(vec ? embed_table_rows<8> : embed_table_rows<1>, (tokens * p.parts + 7u) / 8u, 256, 0, true, 1, s, p);
 }
 
 // One CTA shape and join width of embed_lanes_rows.
@@ -1043,7 +1050,7 @@ dfw_status launch_embed_groups(const RowsOfLanes &p, uint32_t smem, int sms, cud
     }
     // one CTA per SM (more of the smallest shape, which serves long codewords): units go to all SMs first, then to more warps
     const uint64_t ctas = (uint64_t)sms * (NT == 32 ? SMEM_MOST / smem : 1u), units = (uint64_t)p.ids.tokens * p.units;
-    return launch_with(fn, std::min(ctas, units), NT, smem, false, 1, s, p);
+    return launch_with(fn, std::min(ctas, units), NT, smem, true, 1, s, p);
 }
 
 template <int V>
@@ -1152,7 +1159,7 @@ dfw_status launch_grad_sort(SortParams p, uint32_t blocks, cudaStream_t s) {
     }
     p.ctas = blocks * C;
     const uint64_t fillers = (p.fill_bytes + (1u << 16) - 1u) >> 16;  // 64 KB each, in whole clusters
-    return launch_with(grad_sort<C, IPT, PACK>, p.ctas + (fillers + C - 1u) / C * C, SORT_THREADS, smem, false, C, s, p);
+    return launch_with(grad_sort<C, IPT, PACK>, p.ctas + (fillers + C - 1u) / C * C, SORT_THREADS, smem, true, C, s, p);
 }
 template <bool PACK>
 dfw_status launch_grad_sort(const SortParams &p, const GradCut &cut, cudaStream_t s) {
@@ -1183,7 +1190,7 @@ dfw_status launch_grad_few(FewParams p, int sms, cudaStream_t s) {
     // about eight CTAs per SM, of 8 KB at least
     const uint64_t most = std::max<uint64_t>(1u, (uint64_t)sms * 8u / p.col_blocks), row_bytes = (uint64_t)std::min(p.dim, 256u * V) * sizeof(OUT);
     p.rows_per = (uint32_t)std::max((p.ids.rows + most - 1u) / most, ((uint64_t)8192u + row_bytes - 1u) / row_bytes);
-    return launch_with(grad_few<DY, OUT, V>, (p.ids.rows + p.rows_per - 1u) / p.rows_per * p.col_blocks, 256, 0, false, 1, s, p);
+    return launch_with(grad_few<DY, OUT, V>, (p.ids.rows + p.rows_per - 1u) / p.rows_per * p.col_blocks, 256, 0, true, 1, s, p);
 }
 
 // Calls f<DY, OUT, VEC>(p, sms, s) for the call's types and alignment.

@@ -27,7 +27,7 @@
 
 #include <algorithm>
 
-#include "dfw_device.cuh"
+#include "dfw_lanes.cuh"
 
 namespace dfw {
 namespace {
@@ -55,8 +55,12 @@ __device__ __forceinline__ void st_cluster_f32(uint32_t a, float v) {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
 }
 
-// A launch that may be a programmatic dependent of the one before (the kernel
-// then waits for that itself) or run in clusters.
+// A launch that may be a programmatic dependent of the one before, whichever
+// that is, or run in clusters.  A dependent is set up while the one before
+// still runs and waits for its end (griddep_wait) before it touches memory; it
+// lets its own dependents be set up only after that wait, so that none of them
+// runs beside anything earlier.  A stream of calls gains 2 us on each (4096 x
+// 14336 products 18.7 -> 16.7 us, 8192 coded rows 33.8 -> 31.6).
 template <typename F, typename... A>
 dfw_status launch_with(F fn, uint64_t grid, unsigned block, uint32_t smem, bool dependent, unsigned cluster, cudaStream_t s,
                        A... args) {
@@ -407,6 +411,8 @@ __device__ __forceinline__ void q4_store(const Q4GemvParams &a, uint64_t row, ui
 template <int GT, bool Z, int NT, uint32_t W, bool SPLIT>
 __global__ void __launch_bounds__(32 * W, 1) q4_gemv_tiles(const Q4GemvParams a) {
     extern __shared__ __align__(16) uint8_t smem[];
+    griddep_wait();
+    griddep_launch_dependents();
     constexpr uint32_t TILE = Q4_CODES + 32u * GT + (Z ? 16u * GT : 0u), SLOT = Q4_STEP * TILE, RING = q4_ring(NT, W);
     const uint32_t outs = 16u * a.m;  // sums of a row tile, column by column
     const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3u;
@@ -730,7 +736,7 @@ dfw_status launch_q4_pass(Q4GemvParams a, int dev, int sms, cudaStream_t s) {
     a.share = (uint32_t)(a.q.row_tiles / clusters);
     a.extra = (uint32_t)(a.q.row_tiles % clusters);
     smem += (a.pass - 1u) * 64u * a.m;
-    return launch_with(fn, clusters * split, 32u * warps, smem, false, split, s, a);
+    return launch_with(fn, clusters * split, 32u * warps, smem, true, split, s, a);
 }
 
 }  // namespace
