@@ -321,6 +321,60 @@ def test_gradient_accumulates(rows, dim, tokens, spread):
             check_grad(torch.where(hit.cuda()[:, None], out, 0.0).to(dtype), ids, dy, rows, 3.0, torch.where(hit.cuda()[:, None], base, 0.0))
 
 
+@pytest.mark.parametrize("tokens", [40, 3000])
+def test_what_padding_tokens_hold_is_not_read(tokens):
+    ids = grad_ids(50, tokens, "any", 8)
+    dy = torch.randn(tokens, 24, device="cuda")
+    want = dfw.embed_grad(ids.cuda(), dy, 50)
+    for bad in (float("nan"), float("inf"), torch.finfo(torch.float32).min):
+        dy[(ids < 0).cuda()] = bad
+        assert torch.equal(dfw.embed_grad(ids.cuda(), dy, 50), want)
+    t = int(torch.nonzero(ids >= 0)[3])
+    dy[t, 5] = float("nan")  # and a NaN that counts stays in its row and column
+    got = dfw.embed_grad(ids.cuda(), dy, 50)
+    assert got.isnan().sum() == 1 and got[int(ids[t]), 5].isnan()
+
+
+def test_calls_that_follow_each_other_without_a_gap():
+    """Each call reads what the one before wrote, or overwrites what it reads;
+    the launches overlap, the results are those of calls with the GPU idle
+    between them."""
+    gen = torch.Generator("cuda").manual_seed(9)
+    rows, dim, tokens = 3000, 2048, 5000
+    emb = (torch.randn(rows, dim, generator=gen, device="cuda") * 0.02).to(torch.bfloat16)
+    dl = dfw.encode_device(emb)
+    w = dfw.q4_quantise((torch.randn(dim, dim, generator=gen, device="cuda") * 0.02).to(torch.bfloat16))
+    ids = ids_for(rows, tokens).cuda()
+    few = ids[:16].contiguous()
+
+    def chain(wait):
+        table = torch.empty(rows, dim, dtype=torch.bfloat16, device="cuda")
+        kept, pause = [], (torch.cuda.synchronize if wait else lambda: None)
+        for step in range(6):
+            dfw.decode_lanes(dl, out=table.view(-1))
+            pause()
+            x = dfw.embed_rows(table, ids, scale=0.5 + step)
+            pause()
+            y = dfw.q4_gemv(w, dfw.embed_rows(table, few), out_dtype=torch.bfloat16)
+            pause()
+            for _ in range(3):
+                y = dfw.q4_gemv(w, y, out_dtype=torch.bfloat16)
+                pause()
+            dfw.embed_grad(ids, x, rows, out=table)  # overwrites the table that the lookups read
+            pause()
+            z = dfw.embed_rows(table, few)
+            pause()
+            dfw.embed_grad(few, y, rows, out=table, accumulate=True)
+            pause()
+            kept += [x, y, z, table.clone()]
+        torch.cuda.synchronize()
+        return kept
+
+    want = chain(True)
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(chain(False), want))
+
+
 def test_gradient_is_the_difference_quotient():
     """f(E) = sum of c * lookup(E): linear in E, so (f(E + h e) - f(E)) / h is
     the gradient exactly when all values are whole numbers."""
