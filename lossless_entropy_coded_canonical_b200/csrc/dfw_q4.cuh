@@ -106,6 +106,12 @@ __device__ __forceinline__ uint32_t q4_word_at(uint32_t r, uint32_t c) {
     return 512u * (r >> 3) + 16u * (4u * (r & 7u) + ((c >> 3) & 3u)) + 4u * (c >> 5);
 }
 
+__device__ __forceinline__ uint4 ldg_stream(const void *p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+
 // Eight codes in column order (column i in bits 4 i .. 4 i + 3) -> even ones
 // in the low half, odd ones in the high half.
 __device__ __forceinline__ uint32_t q4_split(uint32_t w) {
@@ -117,21 +123,28 @@ __device__ __forceinline__ uint32_t q4_split(uint32_t w) {
 
 // Row-major codes (two to a byte, even column in the low half), scales and
 // zero points -> tiles.  One thread per word of codes; the first threads of a
-// tile also place its scales and zero points.
+// tile also place its scales and zero points.  (Here and in the next two a
+// CTA walks tiles of one row tile: dividing a running tile number cost 0.3 to
+// 0.7 ms on 128256 x 4096.)  Bound by HBM: 128256 x 4096
+// takes 142 us, 3.8 TB/s read and written.
 __global__ void __launch_bounds__(256) q4_pack_tiles(const uint8_t *__restrict__ codes,
                                                      const uint16_t *__restrict__ scales,
                                                      const uint8_t *__restrict__ zeros, const Q4Params p,
                                                      uint8_t *__restrict__ out) {
-    const uint32_t groups = p.cols * p.gt / Q4_COLS;
-    for (uint64_t tile = blockIdx.x; tile < p.row_tiles * p.col_tiles; tile += gridDim.x) {
-        const uint64_t r0 = tile / p.col_tiles * Q4_ROWS;
-        const uint32_t c0 = (uint32_t)(tile % p.col_tiles) * Q4_COLS;
-        uint8_t *dst = out + tile * p.tile_bytes;
-        const uint32_t r = threadIdx.x >> 4, c = 8u * (threadIdx.x & 15u);
-        uint32_t word = p.zeros ? 0u : 0x88888888u;
-        if (r0 + r < p.rows && c0 + c < p.cols)
-            word = q4_split(__ldg(reinterpret_cast<const uint32_t *>(codes + ((r0 + r) * p.cols + c0 + c) / 2u)));
-        *reinterpret_cast<uint32_t *>(dst + q4_word_at(r, c)) = word;
+    const uint32_t groups = p.cols * p.gt / Q4_COLS, r = threadIdx.x >> 4, c = 8u * (threadIdx.x & 15u);
+    const uint64_t r0 = (uint64_t)blockIdx.x * Q4_ROWS;
+    auto load = [&](uint32_t ct) {
+        const uint32_t col = ct * Q4_COLS + c;
+        if (ct >= p.col_tiles || r0 + r >= p.rows || col >= p.cols) return p.zeros ? 0u : 0x88888888u;
+        return __ldg(reinterpret_cast<const uint32_t *>(codes + ((r0 + r) * p.cols + col) / 2u));
+    };
+    uint32_t next = load(blockIdx.y), after = load(blockIdx.y + gridDim.y);
+    for (uint32_t ct = blockIdx.y; ct < p.col_tiles; ct += gridDim.y) {
+        const uint32_t c0 = ct * Q4_COLS, word = next;
+        next = after;
+        after = load(ct + 2u * gridDim.y);
+        uint8_t *dst = out + (blockIdx.x * (uint64_t)p.col_tiles + ct) * p.tile_bytes;
+        *reinterpret_cast<uint32_t *>(dst + q4_word_at(r, c)) = q4_split(word);
         if (threadIdx.x < Q4_ROWS * p.gt) {
             const uint32_t rr = threadIdx.x / p.gt, gi = threadIdx.x % p.gt;
             const uint32_t gr = c0 * p.gt / Q4_COLS + gi;
@@ -143,64 +156,85 @@ __global__ void __launch_bounds__(256) q4_pack_tiles(const uint8_t *__restrict__
     }
 }
 
-// bf16 weights -> tiles.  A warp takes a row's 128 columns, lane l columns
-// 4 l .. 4 l + 3; a group's 32 / GT lanes find its extremes by shuffles.  The
-// quotients are correctly rounded fp32 divisions, so the codes are those of
-// the formula in include/dfw.h whatever the order of work.
-__global__ void __launch_bounds__(512) q4_quantise_tiles(const uint16_t *__restrict__ w, uint64_t ldw, uint32_t vec,
+// w / s rounded to the nearest whole number, ties to even, from r ~ 1 / s.
+// Both are bf16: the quotient is a tie exactly or at least 1/1020 from one, so
+// rounding the product to a multiple of 2^-11 first (by adding 6144) makes
+// ties of ties and moves nothing across one; adding 1.5 2^23 then rounds to a
+// whole number in the sum's low bits.  Where 1 / s overflows, divide.
+template <bool DIVIDE>
+__device__ __forceinline__ int q4_round(float w, float s, float r) {
+    const float t = DIVIDE ? w / s : __fsub_rn(__fmaf_rn(w, r, 6144.f), 6144.f);
+    return __float_as_int(__fadd_rn(t, 12582912.f)) - 0x4B400000;
+}
+template <bool DIVIDE>
+__device__ __forceinline__ uint32_t q4_codes(const uint32_t (&u)[4], float s, float r, int zp) {
+    uint32_t word = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {  // the word's halves hold the even and the odd columns
+        const int a = min(max(q4_round<DIVIDE>(__uint_as_float(u[i] << 16), s, r) + zp, 0), 15);
+        const int b = min(max(q4_round<DIVIDE>(__uint_as_float(u[i] & 0xFFFF0000u), s, r) + zp, 0), 15);
+        word |= (uint32_t)a << (4 * i) | (uint32_t)b << (4 * i + 16);
+    }
+    return word;
+}
+
+// The larger of two bf16 in both halves, NaN if either is.
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// bf16 weights -> tiles.  A thread takes a word's eight columns, sixteen
+// threads a row of a tile, 16 / GT of them a group, whose extremes they find
+// by shuffles.  The codes are those of the formula in include/dfw.h.  Bound by
+// instructions: 128256 x 4096 takes 506 us, 2.6 TB/s read and written, against
+// 709 with the extremes of a thread's weights found in fp32 and the choice
+// between product and division made per weight, 1384 with a division per weight.
+__global__ void __launch_bounds__(256) q4_quantise_tiles(const uint16_t *__restrict__ w, uint64_t ldw, uint32_t vec,
                                                          const Q4Params p, uint8_t *__restrict__ out) {
-    const uint32_t lane = threadIdx.x & 31u, r = threadIdx.x >> 5;
-    const uint32_t span = 32u / p.gt;  // lanes per group
-    for (uint64_t tile = blockIdx.x; tile < p.row_tiles * p.col_tiles; tile += gridDim.x) {
-        const uint64_t row = tile / p.col_tiles * Q4_ROWS + r;
-        const uint32_t col = (uint32_t)(tile % p.col_tiles) * Q4_COLS + 4u * lane;
-        const bool in = row < p.rows && col < p.cols;
-        float v[4] = {0.f, 0.f, 0.f, 0.f};
-        if (in) {
-            const uint16_t *src = w + row * ldw + col;
-            uint32_t u[4];
-            if (vec) {
-                const uint2 q = __ldg(reinterpret_cast<const uint2 *>(src));
-                u[0] = q.x << 16, u[1] = q.x & 0xFFFF0000u, u[2] = q.y << 16, u[3] = q.y & 0xFFFF0000u;
-            } else {
+    const uint32_t r = threadIdx.x >> 4, c = 8u * (threadIdx.x & 15u), span = 16u / p.gt;  // threads per group
+    const uint64_t row = (uint64_t)blockIdx.x * Q4_ROWS + r;
+    auto load = [&](uint32_t ct) {
+        const uint32_t col = ct * Q4_COLS + c;
+        if (ct >= p.col_tiles || row >= p.rows || col >= p.cols) return make_uint4(0u, 0u, 0u, 0u);
+        const uint16_t *src = w + row * ldw + col;
+        if (vec) return ldg_stream(src);
+        uint32_t e[8];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) u[i] = (uint32_t)__ldg(src + i) << 16;
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(u[i]);
-        }
-        float lo = 0.f, hi = 0.f;
-        bool bad = false;
+        for (int i = 0; i < 8; ++i) e[i] = __ldg(src + i);
+        return make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
+    };
+    uint4 next = load(blockIdx.y);
+    for (uint32_t ct = blockIdx.y; ct < p.col_tiles; ct += gridDim.y) {
+        const uint4 cur = next;
+        next = load(ct + gridDim.y);
+        const bool in = row < p.rows && ct * Q4_COLS + c < p.cols;
+        const uint32_t u[4] = {cur.x, cur.y, cur.z, cur.w};
+        uint32_t up = 0u, down = 0u;  // the largest w and the largest -w, at least 0, of the even and odd columns
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            lo = fminf(lo, v[i]);
-            hi = fmaxf(hi, v[i]);
-            bad |= !(fabsf(v[i]) <= 3.4e38f);  // infinities and NaN
+            up = max_bf16x2(up, u[i]);
+            down = max_bf16x2(down, u[i] ^ 0x80008000u);
         }
-        for (uint32_t d = 1; d < span; d <<= 1) {
-            lo = fminf(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, d));
-            hi = fmaxf(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, d));
-            bad |= __shfl_xor_sync(0xFFFFFFFFu, (int)bad, d) != 0;
-        }
+        uint32_t most = max_bf16x2(__byte_perm(up, down, 0x5410), __byte_perm(up, down, 0x7632));  // w low, -w high
+        for (uint32_t d = 1; d < span; d <<= 1) most = max_bf16x2(most, __shfl_xor_sync(0xFFFFFFFFu, most, d));
+        const float hi = __uint_as_float(most << 16), lo = -__uint_as_float(most & 0xFFFF0000u);
+        const bool bad = !(hi <= 3.4e38f && lo >= -3.4e38f);  // an infinity or NaN
         const float range = p.zeros ? __fsub_rn(hi / 15.f, lo / 15.f) : fmaxf(hi, -lo) / 7.f;
         const __nv_bfloat16 sb = __float2bfloat16_rn(bad ? __uint_as_float(0x7FC00000u) : range);
-        const float s = __bfloat162float(sb);
+        const float s = __bfloat162float(sb), inv = 1.f / s;
         // a group whose scale is 0 (all zero, or too small for bf16) has codes
         // equal to its zero point; one with a NaN or infinity has scale NaN
-        const bool live = s > 0.f;
-        const float zp = p.zeros ? (live ? fminf(fmaxf(rintf(-lo / s), 0.f), 15.f) : 0.f) : 8.f;
-        uint32_t half = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float q = live ? rintf(v[i] / s) + zp : zp;
-            half |= (uint32_t)fminf(fmaxf(q, 0.f), 15.f) << (16 * (i & 1) + 4 * (i >> 1));
-        }
-        if (!in) half = p.zeros ? 0u : 0x00880088u;
-        const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, half, 1);
-        uint8_t *dst = out + tile * p.tile_bytes;
-        if (!(lane & 1u)) *reinterpret_cast<uint32_t *>(dst + q4_word_at(r, 4u * lane)) = half | (other << 8);
-        if (lane % span == 0u) {
-            const uint32_t gi = lane / span;
+        const bool live = s > 0.f, tiny = s < 0x1p-120f;
+        int zp = p.zeros ? 0 : 8;
+        if (p.zeros && live) zp = min(max(tiny ? q4_round<true>(-lo, s, inv) : q4_round<false>(-lo, s, inv), 0), 15);
+        uint32_t word = (uint32_t)zp * 0x11111111u;
+        if (live) word = tiny ? q4_codes<true>(u, s, inv, zp) : q4_codes<false>(u, s, inv, zp);
+        uint8_t *dst = out + (blockIdx.x * (uint64_t)p.col_tiles + ct) * p.tile_bytes;
+        *reinterpret_cast<uint32_t *>(dst + q4_word_at(r, c)) = in ? word : p.zeros ? 0u : 0x88888888u;
+        if ((threadIdx.x & 15u) % span == 0u) {
+            const uint32_t gi = (threadIdx.x & 15u) / span;
             reinterpret_cast<uint16_t *>(dst + Q4_CODES)[r * p.gt + gi] = in ? __bfloat16_as_ushort(sb) : (uint16_t)0;
             if (p.zeros) dst[Q4_CODES + 32u * p.gt + r * p.gt + gi] = in ? (uint8_t)zp : (uint8_t)0;
         }
@@ -208,14 +242,17 @@ __global__ void __launch_bounds__(512) q4_quantise_tiles(const uint16_t *__restr
 }
 
 // Tiles -> bf16 weights s (q - z), rounded once (the product has 12 bits).
+// Bound by HBM: 128256 x 4096 takes 264 us, 5.0 TB/s read and written.
 __global__ void __launch_bounds__(256) q4_dequantise_tiles(const uint8_t *__restrict__ packed, const Q4Params p,
                                                            uint16_t *__restrict__ out) {
-    for (uint64_t tile = blockIdx.x; tile < p.row_tiles * p.col_tiles; tile += gridDim.x) {
-        const uint32_t r = threadIdx.x >> 4, c = 8u * (threadIdx.x & 15u);
-        const uint64_t row = tile / p.col_tiles * Q4_ROWS + r;
-        const uint32_t col = (uint32_t)(tile % p.col_tiles) * Q4_COLS + c;
-        if (row >= p.rows || col >= p.cols) continue;
-        const uint8_t *src = packed + tile * p.tile_bytes;
+    const uint32_t r = threadIdx.x >> 4, c = 8u * (threadIdx.x & 15u);
+    const uint64_t row = (uint64_t)blockIdx.x * Q4_ROWS + r;
+    if (row >= p.rows) return;
+#pragma unroll 2
+    for (uint32_t ct = blockIdx.y; ct < p.col_tiles; ct += gridDim.y) {
+        const uint32_t col = ct * Q4_COLS + c;
+        if (col >= p.cols) break;
+        const uint8_t *src = packed + (blockIdx.x * (uint64_t)p.col_tiles + ct) * p.tile_bytes;
         const uint32_t word = __ldg(reinterpret_cast<const uint32_t *>(src + q4_word_at(r, c)));
         const uint32_t gi = c * p.gt / Q4_COLS;
         const float s = __uint_as_float((uint32_t)reinterpret_cast<const uint16_t *>(src + Q4_CODES)[r * p.gt + gi] << 16);
@@ -614,9 +651,10 @@ dfw_status device_sms(int &sms) {
     return DFW_OK;
 }
 
-unsigned q4_grid(const Q4Params &p, int sms, unsigned per_sm) {
-    const uint64_t tiles = p.row_tiles * p.col_tiles, cap = (uint64_t)sms * per_sm;
-    return (unsigned)(tiles < cap ? tiles : cap);
+// A CTA per row tile, several where there are few row tiles.
+dim3 q4_grid(const Q4Params &p, int sms) {
+    const uint64_t want = ((uint64_t)sms * 16u + p.row_tiles - 1u) / p.row_tiles;
+    return dim3((unsigned)p.row_tiles, (unsigned)std::min<uint64_t>(want, p.col_tiles));
 }
 
 }  // namespace
@@ -630,7 +668,7 @@ dfw_status launch_q4_pack(const uint8_t *d_codes, const uint16_t *d_scales, cons
     if (!d_codes || !d_scales || (d_zeros != nullptr) != (p.zeros != 0u)) return DFW_EINVAL;
     if ((reinterpret_cast<uintptr_t>(d_codes) & 3u) || (reinterpret_cast<uintptr_t>(d_scales) & 1u)) return DFW_EALIGN;
     if ((st = device_sms(sms)) != DFW_OK) return st;
-    q4_pack_tiles<<<q4_grid(p, sms, 8), 256, 0, s>>>(d_codes, d_scales, d_zeros, p, d_packed);
+    q4_pack_tiles<<<q4_grid(p, sms), 256, 0, s>>>(d_codes, d_scales, d_zeros, p, d_packed);
     return cudaGetLastError() == cudaSuccess ? DFW_OK : DFW_ECUDA;
 }
 
@@ -642,9 +680,9 @@ dfw_status launch_q4_quantise(const uint16_t *d_w, uint64_t ldw, const dfw_q4_in
     if (st != DFW_OK) return st;
     if (!d_w || ldw < p.cols) return DFW_EINVAL;
     if (reinterpret_cast<uintptr_t>(d_w) & 1u) return DFW_EALIGN;
-    const uint32_t vec = (reinterpret_cast<uintptr_t>(d_w) & 7u) == 0u && ldw % 4u == 0u;
+    const uint32_t vec = (reinterpret_cast<uintptr_t>(d_w) & 15u) == 0u && (p.rows == 1u || ldw % 8u == 0u);
     if ((st = device_sms(sms)) != DFW_OK) return st;
-    q4_quantise_tiles<<<q4_grid(p, sms, 4), 512, 0, s>>>(d_w, ldw, vec, p, d_packed);
+    q4_quantise_tiles<<<q4_grid(p, sms), 256, 0, s>>>(d_w, ldw, vec, p, d_packed);
     return cudaGetLastError() == cudaSuccess ? DFW_OK : DFW_ECUDA;
 }
 
@@ -656,7 +694,7 @@ dfw_status launch_q4_dequantise(const uint8_t *d_packed, const dfw_q4_info *info
     if (!d_out) return DFW_EINVAL;
     if (reinterpret_cast<uintptr_t>(d_out) & 15u) return DFW_EALIGN;
     if ((st = device_sms(sms)) != DFW_OK) return st;
-    q4_dequantise_tiles<<<q4_grid(p, sms, 8), 256, 0, s>>>(d_packed, p, d_out);
+    q4_dequantise_tiles<<<q4_grid(p, sms), 256, 0, s>>>(d_packed, p, d_out);
     return cudaGetLastError() == cudaSuccess ? DFW_OK : DFW_ECUDA;
 }
 

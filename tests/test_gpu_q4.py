@@ -252,3 +252,20 @@ def test_repeats_streams_and_graphs():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, want[1] * scale)  # a power of two: exact
+
+
+def test_quantise_rounds_every_pair_of_bf16_significands():
+    """Every quotient a / b of 8-bit significands, at six powers of two: ties
+    and the quotients next to them, with scales down to the smallest bf16."""
+    a = torch.arange(128, 256, dtype=torch.float64)
+    for shift in (-6, -3, -2, -1, 0, 1):
+        for expo in (-9, 100, -132):  # of the scale: ordinary, large, below the normal range
+            # column 0 of a row fixes the scale at b 2^expo: 7 times it, exactly a bf16 or not, is rounded back to it
+            b = torch.arange(128, 256, dtype=torch.float64)
+            w = torch.zeros(128, 160, dtype=torch.float64)
+            w[:, 0] = 7 * b * 2.0 ** (expo - 7)
+            w[:, 1:129] = a[None, :] * 2.0 ** (shift + expo - 7)
+            w = w.clamp(max=3e38).to(torch.bfloat16)
+            q, s, z = quantised(w.double().numpy(), 32, False)
+            got = dfw.q4_quantise(w.cuda(), group=32)
+            assert torch.equal(got.packed, to_gpu(q, s, z, 32).packed), (shift, expo)
