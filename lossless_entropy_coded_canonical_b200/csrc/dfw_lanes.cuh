@@ -465,17 +465,21 @@ __global__ void __launch_bounds__(NT) decode_lanes(const LanesParams prm, const 
     }
     __syncthreads();  // the barriers are initialised
     bool tok = mbar_wait(bar_t, 0u);
+    // (a launch chained after another never ends before that one, not even
+    // without decoding: what follows it on the stream waits for it alone)
     if (!__syncthreads_and(tok)) {  // the table copy never completed: give up
         if (tid == 0) {
             atomicOr(&g_status, ST_TIMEOUT);
             mbar_wait_bounded(bar_t, 0u);
         }
+        if (prm.wait_prior) griddep_wait();
         return;
     }
     // check every entry; escapes get the loop's escape word
     const bool bad = check_fast_table<NT>(s_fast, n_fast, prm.fast_bits, tid);
     if (__syncthreads_or(bad)) {
         if (tid == 0) atomicOr(&g_status, ST_LUT);
+        if (prm.wait_prior) griddep_wait();
         return;
     }
     if (!active) return;  // no CTA barrier follows
@@ -567,6 +571,7 @@ __global__ void __launch_bounds__(NT) decode_lanes(const LanesParams prm, const 
                 mbar_wait_bounded(bar_m, k & 1u);
                 if (has_next) mbar_wait_bounded(bar_s0 + 8u * (s ^ 1u), ((k + 1) >> 1) & 1u);
             }
+            if (prm.wait_prior) griddep_wait();
             return;
         }
         const bool good = valid && !__any_sync(0xFFFFFFFFu, err != 0u);

@@ -213,6 +213,23 @@ def test_a_damaged_plan_is_reported(tokens):
         assert (out == 9.0).all(), damage  # a damaged group writes nothing
 
 
+def test_rows_of_a_decode_whose_last_scope_is_damaged():
+    """The last launch of a sequence finds its table malformed and decodes
+    nothing; what follows it must still wait for the launches before it."""
+    u = table(20000 * 2048)
+    scopes = [coded(u)] * 40 + [coded(table(2048))]  # a launch takes 40
+    scopes[-1].lut.fill_(-1)
+    assert dfw.decode_lanes_seq_launches(scopes) == 2
+    ids = torch.arange(19999, 0, -7, dtype=torch.int64, device="cuda")
+    want = rows_of(u, 0, 20000, 2048, ids.cpu(), 1.0)
+    for _ in range(3):
+        out = torch.zeros(20000, 2048, dtype=torch.bfloat16, device="cuda")
+        dfw.decode_lanes_seq(scopes, out.view(-1))
+        rows = dfw.embed_rows(out, ids)
+        assert dfw.status_bits() == (dfw.ECORRUPT, dfw.ST_LUT)
+        assert same(rows, want)
+
+
 # ------------------------------------------------------------------ gradient
 
 def grad_of(ids, dy, rows, scale):
