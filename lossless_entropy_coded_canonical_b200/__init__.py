@@ -569,6 +569,10 @@ class Q4Weights:
     packed: torch.Tensor  # uint8[info.bytes]
     info: Q4Info
 
+    def __post_init__(self):
+        if self.packed.dtype != torch.uint8 or not self.packed.is_contiguous() or self.packed.numel() != self.info.bytes:
+            raise ValueError(f"packed must be a contiguous uint8 tensor of {self.info.bytes} bytes")
+
     @property
     def shape(self) -> tuple[int, int]:
         return int(self.info.rows), int(self.info.cols)

@@ -493,3 +493,25 @@ def test_lookup_products_and_a_training_step_together():
     every = torch.arange(rows, device="cuda", dtype=torch.int32)
     assert torch.equal(dfw.embed_lanes(again, every, dim), new)
     assert torch.equal(new[[1, 2, 3]], emb[[1, 2, 3]]) and not torch.equal(new[5], emb[5])
+
+
+def test_offsets_past_32_bits():
+    """Rows and gradient rows past element 2^32: 2^20 tokens of 4104."""
+    rows, dim, tokens = 100, 4104, 1 << 20
+    u = table(rows * dim, seed=9)
+    ids = torch.randint(0, rows, (tokens,), device="cuda", generator=torch.Generator(device="cuda").manual_seed(2))
+    w = torch.from_numpy(u.view(np.int16)).view(torch.bfloat16).view(rows, dim).cuda()
+    out = torch.empty(tokens, dim, dtype=torch.bfloat16, device="cuda")
+    for look in (lambda: dfw.embed_rows(w, ids, out=out), lambda: dfw.embed_lanes(coded(u), ids, dim, out=out)):
+        out.fill_(7.0)
+        look()
+        for at in (slice(0, 1000), slice(tokens // 2 - 500, tokens // 2 + 500), slice(tokens - 1000, tokens)):
+            assert torch.equal(out[at], w[ids[at]])
+    out[:, 1:-1] = 0.0  # whole numbers in the first and the last column
+    out[:, 0] = (torch.arange(tokens, device="cuda") % 5).to(torch.bfloat16)
+    out[:, -1] = (torch.arange(tokens, device="cuda") % 3).to(torch.bfloat16)
+    grad = dfw.embed_grad(ids, out, rows)
+    for col in (0, dim - 1):
+        want = torch.zeros(rows, dtype=torch.float64, device="cuda").index_add_(0, ids, out[:, col].double())
+        assert torch.equal(grad[:, col].double(), want)
+    assert not grad[:, 1:-1].any()

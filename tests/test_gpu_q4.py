@@ -269,3 +269,62 @@ def test_quantise_rounds_every_pair_of_bf16_significands():
             q, s, z = quantised(w.double().numpy(), 32, False)
             got = dfw.q4_quantise(w.cuda(), group=32)
             assert torch.equal(got.packed, to_gpu(q, s, z, 32).packed), (shift, expo)
+
+
+def test_a_captured_call_behind_a_copy_a_fill_and_another_stream():
+    """What precedes a call inside a graph need not be a kernel, nor one thing."""
+    q, s, z = make(500, 1024, 64, True, seed=5, whole=True)
+    qw = to_gpu(q, s, z, 64)
+    src, ids = vectors(3, 1024, seed=6, whole=True).cuda(), torch.tensor([2, 0, 1], device="cuda")
+    want = src.double().cpu() @ torch.from_numpy(weights(q, s, z, 64)).T
+    x, y1, y2 = torch.empty_like(src), torch.empty(3, 500, device="cuda"), torch.empty(3, 500, device="cuda")
+    picked, grad = torch.empty_like(src), torch.empty(3, 1024, device="cuda")
+    side = torch.cuda.Stream()
+
+    def calls():
+        x.copy_(src)  # a copy, then a product
+        dfw.q4_gemv(qw, x, out=y1)
+        y2.zero_()  # a fill, then a product on each of two streams
+        side.wait_stream(torch.cuda.current_stream())
+        dfw.q4_gemv(qw, x, out=y2, stream=side)
+        dfw.embed_rows(x, ids, out=picked)
+        torch.cuda.current_stream().wait_stream(side)
+        return dfw.embed_grad(ids, picked, 3, out=grad)  # behind both streams
+
+    calls()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        calls()
+    for scale in (1.0, 2.0):
+        src.mul_(scale)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y1.double().cpu(), want * scale) and torch.equal(y2, y1)
+        assert torch.equal(picked, src[ids]) and torch.equal(grad, src.float())
+    dfw.check()
+
+
+def test_offsets_past_32_bits():
+    """A matrix of 9.2e9 weights in 4.7 GB, all zero but for its ends."""
+    rows, cols = 140001, 65536
+    w = torch.zeros(rows, cols, dtype=torch.bfloat16, device="cuda")
+    rng = torch.Generator(device="cuda").manual_seed(3)
+    for part in (w[:5], w[-20:]):
+        part.copy_(torch.randint(-7, 8, part.shape, generator=rng, device="cuda"))
+        part[:, ::128] = 7  # scale 1: the codes are the weights
+    q = dfw.q4_quantise(w)
+    assert q.packed.numel() > 1 << 32
+    x = torch.randint(-2, 3, (2, cols), generator=rng, device="cuda").to(torch.bfloat16)
+    y = dfw.q4_gemv(q, x)
+    for part in (slice(0, 5), slice(rows - 20, rows)):
+        assert torch.equal(y[:, part].double(), x.double() @ w[part].double().T)
+    assert not y[:, 5:-20].any()
+    back = dfw.q4_dequantise(q)
+    assert torch.equal(back[:5], w[:5]) and torch.equal(back[-20:], w[-20:]) and not back[5:-20].any()
+    del back, w
+    codes = torch.full((rows, cols // 2), 0x88, dtype=torch.uint8, device="cuda")
+    scales = torch.zeros(rows, cols // 128, dtype=torch.bfloat16, device="cuda")
+    codes[-1, -1], scales[-1, -1] = 0xF8, 2.0
+    y = dfw.q4_gemv(dfw.q4_pack(codes, scales), torch.ones(cols, dtype=torch.bfloat16, device="cuda"))
+    assert y[-1] == 14.0 and not y[:-1].any()

@@ -150,3 +150,12 @@ def test_binding_refuses_host_tensors_and_types():
         dfw.embed_rows(w, torch.zeros(3, dtype=torch.int64))
     with pytest.raises(ValueError):
         dfw.embed_grad(torch.zeros(3, dtype=torch.int64), torch.zeros(3, 8), 5)
+
+
+def test_packed_weights_must_be_what_their_info_says():
+    info = q4_info(33, 256, 64, 1)
+    whole = torch.zeros(info.bytes + 16, dtype=torch.uint8)
+    assert dfw.Q4Weights(whole[:info.bytes], info).shape == (33, 256)
+    for packed in (whole, whole[:info.bytes - 1], whole[:info.bytes].view(torch.int8), torch.zeros(info.bytes * 2, dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError):
+            dfw.Q4Weights(packed, info)
