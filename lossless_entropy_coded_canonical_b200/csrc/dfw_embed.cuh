@@ -147,7 +147,7 @@ struct RowsOfLanes {
     uint16_t *out;
     uint64_t ldo;
     uint32_t dim;
-    uint32_t units;        // units a token's row is cut into: its groups if rows are whole groups or parts of one, else 1
+    uint32_t units;        // the most groups a row meets
     uint32_t single;       // total_bits == 0: every exponent is this one
     RowScale scale;
 };
@@ -173,7 +173,7 @@ __device__ __forceinline__ void join_row(const RowScale &s, uint16_t *out, uint3
             stg256_cs(out + i, scaled8<KIND>(a, s), scaled8<KIND>(b, s));
         }
     } else if constexpr (V == 8) {
-#pragma unroll
+#pragma unroll 4
         for (uint32_t j = 0; j < 8u; ++j) {  // piece lane + 32 j: words 2 (piece mod 8) and + 1 of chunk piece / 8
             const uint32_t piece = lane + 32u * j, i = 8u * piece;
             if (i < lo || i >= hi || !check(i + V <= hi, CK_EMBED_STORE)) continue;
@@ -193,16 +193,21 @@ __device__ __forceinline__ void join_row(const RowScale &s, uint16_t *out, uint3
     }
 }
 
-// The decode kernel's work on chosen groups: a warp takes the groups of a
-// token's row in turn (in units of a group where every row is whole groups or
-// lies in one), staged as decode_lanes stages its own (the same copies,
-// positions, lookups and checks), except that lanes whose chunk the row does
-// not touch decode nothing, and the join scales and writes the row's part of
-// the group.  The id of the unit after the next and the starts of the group
-// after the current one are loaded ahead; the table's copy and check overlap
-// the first group's three dependent loads (id, group start, stream).
-// Bound by instruction issue, as the decode: 8192 rows of 4096 take 32 us, 0.20
-// per group and SM past 10 of start; one row 6.6, a chain of dependent loads.
+// The decode kernel's work on chosen groups: a unit is one group of a token's
+// row (the first ones of all tokens, then the second ones; rows that begin
+// anywhere meet fewer groups than others, and those units are passed over),
+// staged as decode_lanes stages its own (the same copies, positions, lookups
+// and checks), except that lanes whose chunk the row does not touch decode
+// nothing, and the join scales and writes the row's part of the group.  (Rows
+// that are not whole groups as one unit each: 3 rows of 20000 32 us, so 7; 67
+// of 5365 17.7 and 8.5; 2000 of 5365 27 and 24; 8000 of 1000 21.6 and 21.5;
+// 4000 of 1001 15.4 and 17.)
+// The starts of the group after the current one are loaded ahead; the table's
+// copy and check overlap the first group's three dependent loads (id, group
+// start, stream).
+// Bound by instruction issue, as the decode: 8192 rows of 4096 take 29.3 us,
+// 0.18 per group and SM past 10 of start (32 us with a unit's id loaded by
+// itself); one row 6.1, a chain of dependent loads.
 // V: the join's weights per access; every row begins at a multiple of V in
 // the scope and at 2 V bytes in the output (V = 1: no alignment).
 template <int NT, int V>
@@ -238,46 +243,38 @@ __global__ void __launch_bounds__(NT) embed_lanes_rows(const RowsOfLanes p) {
 
     // a group of a token's row
     struct Item {
-        uint64_t w0;          // the row's first weight
-        uint64_t s0, s1;      // the group's bits
-        uint32_t t, g, last;  // token, group, the unit's last group
+        uint64_t s0, s1;  // the group's bits
+        uint32_t t, g;    // token, group
+        int32_t from;     // the row's first weight, from the group's
     };
-    // this warp's units: token `at_t`, part `part` of its row, then every
-    // `stride` units further (t_step tokens and p_step parts)
-    const uint32_t stride = gridDim.x * NWARP, t_step = stride / p.units, p_step = stride % p.units;
-    const uint32_t unit0 = warp * gridDim.x + blockIdx.x;
-    uint32_t at_t = unit0 / p.units, part = unit0 % p.units;
-    uint64_t row_ahead = 0;
-    bool have_ahead = at_t < p.ids.tokens && token_row(p.ids, at_t, row_ahead, lane == 0u && part == 0u);
-    // the next group: the unit's next one, or the first of the next unit with a row
-    auto advance = [&](Item &it, bool in_unit) {
-        if (in_unit && it.g < it.last) {
-            ++it.g;
-        } else {
-            for (;;) {
-                if (at_t >= p.ids.tokens) return false;
-                const uint32_t t = at_t, at = part;
-                const bool have = have_ahead;
-                const uint64_t row = row_ahead;
-                at_t += t_step;
-                part += p_step;
-                if (part >= p.units) {
-                    part -= p.units;
-                    ++at_t;
-                }
-                have_ahead = at_t < p.ids.tokens && token_row(p.ids, at_t, row_ahead, lane == 0u && part == 0u);
-                if (!have) {
-                    const uint32_t c0 = at * GROUP_SYMS;
-                    zero_row(p.out + t * p.ldo, c0, at + 1u < p.units ? c0 + GROUP_SYMS : p.dim, lane);
-                    continue;
-                }
-                it.t = t;
-                it.w0 = p.first + row * p.dim;
-                it.g = (uint32_t)(it.w0 / GROUP_SYMS) + at;
-                it.last = p.units > 1u ? it.g : (uint32_t)((it.w0 + p.dim - 1u) / GROUP_SYMS);
-                break;
+    // this warp's units are unit0, unit0 + stride, ...; the lanes look at the
+    // next 32 at once: unit u is group u / tokens of token u mod tokens's row
+    const uint32_t stride = gridDim.x * NWARP, all = p.ids.tokens * p.units;
+    uint32_t next = warp * gridDim.x + blockIdx.x, my_row = 0, my_unit = 0, rows = 0, pads = 0;  // my_unit: token | group << 20
+    auto advance = [&](Item &it) {
+        while (!rows) {
+            for (; pads; pads &= pads - 1u) {
+                const uint32_t unit = __shfl_sync(0xFFFFFFFFu, my_unit, __ffs(pads) - 1), c0 = (unit >> 20) * GROUP_SYMS;
+                zero_row(p.out + (unit & 0xFFFFFu) * p.ldo, c0, min(c0 + GROUP_SYMS, p.dim), lane);
             }
+            if (next >= all) return false;
+            const uint32_t u = next + lane * stride, part = u / p.ids.tokens, t = u - part * p.ids.tokens;
+            next += 32u * stride;
+            uint64_t row = 0;
+            const bool have = u < all && token_row(p.ids, t, row, part == 0u);
+            const uint64_t w0 = p.first + row * p.dim;
+            my_row = (uint32_t)row;
+            my_unit = t | part << 20;
+            rows = __ballot_sync(0xFFFFFFFFu, have && (w0 / GROUP_SYMS + part) * GROUP_SYMS < w0 + p.dim);
+            pads = __ballot_sync(0xFFFFFFFFu, u < all && !have);
         }
+        const int from = __ffs(rows) - 1;
+        rows &= rows - 1u;
+        const uint32_t unit = __shfl_sync(0xFFFFFFFFu, my_unit, from);
+        const uint64_t w0 = p.first + (uint64_t)__shfl_sync(0xFFFFFFFFu, my_row, from) * p.dim;
+        it.t = unit & 0xFFFFFu;
+        it.g = (uint32_t)(w0 / GROUP_SYMS) + (unit >> 20);
+        it.from = (int32_t)(w0 % GROUP_SYMS) - (int32_t)(GROUP_SYMS * (unit >> 20));
         it.s0 = __ldg(prm.group_start + it.g);
         it.s1 = __ldg(prm.group_start + it.g + 1u);
         return true;
@@ -308,13 +305,13 @@ __global__ void __launch_bounds__(NT) embed_lanes_rows(const RowsOfLanes p) {
         if (ok) bulk_load(smem_u32(mbuf), prm.mant + m0, bytes, bar_m);
     };
     Item cur = {}, nxt;
-    bool live = advance(cur, false);
+    bool live = advance(cur);
     if (live && lane == 0u) {
         issue_stream(cur, 0);
         issue_mant(cur);
     }
     nxt = cur;
-    bool more = live && advance(nxt, true);
+    bool more = live && advance(nxt);
 
     __syncthreads();  // the table's barrier is initialised
     const bool tok = mbar_wait(bar_t, 0u);
@@ -353,8 +350,7 @@ __global__ void __launch_bounds__(NT) embed_lanes_rows(const RowsOfLanes p) {
                                                        ((cur.s0 >> 3) & ~15ull) + span <= prm.stream_bytes &&
                                                        (n != 0u || cbits == 0u));
         // the row's weights of the group: [lo, hi) of its 2048
-        const int64_t from = (int64_t)cur.w0 - (int64_t)cur.g * GROUP_SYMS;
-        const uint32_t lo = (uint32_t)max(from, (int64_t)0), hi = (uint32_t)min(from + p.dim, (int64_t)GROUP_SYMS);
+        const uint32_t lo = (uint32_t)max(cur.from, 0), hi = (uint32_t)min(cur.from + (int32_t)p.dim, (int32_t)GROUP_SYMS);
         uint32_t err = 0;
         if (ok && valid && LANE_SYMS * lane < hi && LANE_SYMS * lane + n > lo) {  // the row touches this chunk
             const uint32_t r = r0 + excl;
@@ -366,7 +362,7 @@ __global__ void __launch_bounds__(NT) embed_lanes_rows(const RowsOfLanes p) {
             check(wr_end < exps + EXP_STRIDE * EXP_WORDS, CK_EMBED_READ);
         }
         Item ahead = nxt;
-        const bool ahead_live = more && advance(ahead, true);
+        const bool ahead_live = more && advance(ahead);
         ok = mbar_wait(bar_m, k & 1u) && ok;
         if (!__all_sync(0xFFFFFFFFu, ok)) {  // a bulk copy never completed: give up
             if (lane == 0u) {  // report, then give each copy in flight one more bounded wait
@@ -384,7 +380,7 @@ __global__ void __launch_bounds__(NT) embed_lanes_rows(const RowsOfLanes p) {
             if (err) atomicOr(&g_status, err);
         } else {
             __syncwarp();  // the join reads other lanes' exponent slots
-            uint16_t *out = p.out + (int64_t)(cur.t * p.ldo) + ((int64_t)cur.g * GROUP_SYMS - (int64_t)cur.w0);
+            uint16_t *out = p.out + (int64_t)(cur.t * p.ldo) - cur.from;
             const uint32_t mb = smem_u32(mbuf);
             switch (p.scale.kind) {
                 case SCALE_ONE: join_row<SCALE_ONE, V>(p.scale, out, lo, hi, mb, exps0, lane); break;
@@ -1112,8 +1108,7 @@ dfw_status launch_embed_lanes(const dfw_lanes_scope *scope, uint64_t first, uint
                            false, 1, s, p);
     }
     const bool whole = first % GROUP_SYMS == 0u && (dim % GROUP_SYMS == 0u || GROUP_SYMS % dim == 0u);
-    p.units = whole ? (dim + GROUP_SYMS - 1u) / GROUP_SYMS : 1u;
-    if (tokens * p.units > 0x7FFFFFFFull) return DFW_EINVAL;
+    p.units = (dim + GROUP_SYMS - (whole ? 1u : 2u)) / GROUP_SYMS + (whole ? 0u : 1u);
     if (out32 && first % 16u == 0u && dim % 16u == 0u) return launch_embed_width<16>(p, sms, s);
     if (out16 && first % 8u == 0u && dim % 8u == 0u) return launch_embed_width<8>(p, sms, s);
     return launch_embed_width<1>(p, sms, s);
