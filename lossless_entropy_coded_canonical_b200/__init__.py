@@ -16,6 +16,7 @@ Typical use::
 from __future__ import annotations
 
 import ctypes
+import struct
 from dataclasses import dataclass
 
 import numpy as np
@@ -675,6 +676,10 @@ def q4_gemv(q: Q4Weights, x: torch.Tensor, out: torch.Tensor | None = None, out_
     return out
 
 
+# A LanesScope as the bytes it is, packed in a tenth of the time that building the object takes.
+_scope_bytes = struct.Struct("@7P").pack
+
+
 def _embed_out(ids: torch.Tensor, dim: int, out, dev) -> torch.Tensor:
     _expect("ids", ids, dev, _IDS)
     if not ids.is_contiguous():
@@ -712,9 +717,9 @@ def embed_lanes(dl: DeviceLanes, ids: torch.Tensor, dim: int, scale: float = 1.0
     if rows is None:
         rows = (dl.n - first) // dim if dim > 0 else 0
     out = _embed_out(ids, dim, out, dev)
-    scope = LanesScope(dl.stream.data_ptr(), dl.mant.data_ptr(), dl.lut.data_ptr(), dl.chunk_bits.data_ptr(),
-                       dl.group_start.data_ptr(), ctypes.pointer(dl.table), ctypes.pointer(dl.info))
-    _check(lib().dfw_embed_lanes(ctypes.byref(scope), first, rows, dim, ids.data_ptr(), ids.dtype is torch.int64, ids.numel(),
+    scope = _scope_bytes(dl.stream.data_ptr(), dl.mant.data_ptr(), dl.lut.data_ptr(), dl.chunk_bits.data_ptr(),
+                         dl.group_start.data_ptr(), ctypes.addressof(dl.table), ctypes.addressof(dl.info))
+    _check(lib().dfw_embed_lanes(scope, first, rows, dim, ids.data_ptr(), ids.dtype is torch.int64, ids.numel(),
                                  scale, out.data_ptr(), _pitch(out, dim), sh), "dfw_embed_lanes")
     return out
 
