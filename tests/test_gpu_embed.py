@@ -515,3 +515,17 @@ def test_offsets_past_32_bits():
         want = torch.zeros(rows, dtype=torch.float64, device="cuda").index_add_(0, ids, out[:, col].double())
         assert torch.equal(grad[:, col].double(), want)
     assert not grad[:, 1:-1].any()
+
+
+@pytest.mark.parametrize("rows,dim,tokens", [(7, 96, 40), (50, 96, 400000), (11, 5365, 9000), (4, 20000, 700), (30, 2048, 200000)])
+@pytest.mark.parametrize("every", [0, 1, 3, 4097])
+def test_padding_and_batches_of_many_units(rows, dim, tokens, every):
+    """Only every n-th token (or none) has a row; warps take many more units than they look at once."""
+    u = table(rows * dim, seed=dim)
+    w = torch.from_numpy(u.view(np.int16)).view(torch.bfloat16).view(rows, dim).cuda()
+    ids = torch.full((tokens,), -5, dtype=torch.int32, device="cuda")
+    if every:
+        ids[::every] = (torch.arange(tokens, device="cuda", dtype=torch.int32) * 7 % rows)[::every]
+    want = torch.where((ids >= 0)[:, None], w[ids.clamp(min=0).long()], torch.zeros((), dtype=torch.bfloat16, device="cuda"))
+    for look in (lambda out: dfw.embed_lanes(coded(u), ids, dim, out=out), lambda out: dfw.embed_rows(w, ids, out=out)):
+        assert torch.equal(look(torch.full((tokens, dim), 3.0, dtype=torch.bfloat16, device="cuda")), want)
