@@ -43,10 +43,20 @@ __device__ __forceinline__ bool token_row(const IdSource &s, uint32_t t, uint64_
     return true;
 }
 
-// bf16(scale w), rounded to nearest even, of two weights at a time.  Scale 1
-// keeps the bits (NaN payloads included), as the decoder does.  A scale that is
-// a bf16 itself takes one packed multiplication: the 16-bit products are exact
-// before its one rounding, so the result is the fp32 product's, rounded.
+// a b for a bf16 result, with the bits past fp32's 24 cut off and, if there
+// were any, the lowest one kept set: such a value is on no tie of the 8 bits
+// that a bf16 keeps unless a b itself is, so the conversion to the nearest bf16
+// rounds as if from a b.  (Rounded to the nearest fp32 first, a product just
+// beside a tie can become one: a scale of 24 bits misrounded up to 1 in 130
+// weights.)  A product past the largest fp32 stays past the largest bf16.
+__device__ __forceinline__ float mul_odd(float a, float b) {
+    const float z = __fmul_rz(a, b), away = __fmul_ru(fabsf(a), fabsf(b));
+    return __uint_as_float(__float_as_uint(z) | (fabsf(z) != away ? 1u : 0u));
+}
+
+// bf16(scale w), rounded once to nearest even, of two weights at a time.
+// Scale 1 keeps the bits (NaN payloads included), as the decoder does.  A scale
+// that is a bf16 itself takes one packed multiplication; others go by mul_odd.
 enum ScaleKind { SCALE_ONE, SCALE_BF16, SCALE_FP32 };
 struct RowScale {
     float f;
@@ -65,7 +75,7 @@ __device__ __forceinline__ uint32_t scaled2(uint32_t w, const RowScale &s) {
     if constexpr (KIND == SCALE_BF16) {
         asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(w), "r"(s.pair));
     } else {
-        const float lo = __uint_as_float(w << 16) * s.f, hi = __uint_as_float(w & 0xFFFF0000u) * s.f;
+        const float lo = mul_odd(__uint_as_float(w << 16), s.f), hi = mul_odd(__uint_as_float(w & 0xFFFF0000u), s.f);
         asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     }
     return r;

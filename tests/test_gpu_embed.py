@@ -1,9 +1,9 @@
 """Embedding rows from a coded scope and from a bf16 table, and the table's
 gradient, against plain 64-bit arithmetic.
 
-A row is one rounding of scale x weight (the fp32 product of a scale of at
-most 16 bits and a bf16 weight is exact), so those must be equal bit for bit;
-for a scale of more bits the product is rounded twice, 2^-24 and 2^-8.
+A row is one rounding of scale x weight, so it must be equal bit for bit: the
+fp32 product of a scale of at most 16 bits and a bf16 weight is exact, that of
+a scale of more bits is exact in 64 bits.
 The gradient is a sum of k terms in fp32, in some order: off by at most
 (k + 1) 2^-24 times the scaled sum of magnitudes (one rounding per addition
 and one for the scale), plus 2^-8 of the value for a bf16 result.  Whole
@@ -529,3 +529,45 @@ def test_padding_and_batches_of_many_units(rows, dim, tokens, every):
     want = torch.where((ids >= 0)[:, None], w[ids.clamp(min=0).long()], torch.zeros((), dtype=torch.bfloat16, device="cuda"))
     for look in (lambda out: dfw.embed_lanes(coded(u), ids, dim, out=out), lambda out: dfw.embed_rows(w, ids, out=out)):
         assert torch.equal(look(torch.full((tokens, dim), 3.0, dtype=torch.bfloat16, device="cuda")), want)
+
+
+def once(exact):
+    """64-bit values that are exact, rounded to bf16 in one step, ties to even."""
+    exact = np.asarray(exact, dtype=np.float64)
+    step = np.exp2(np.maximum(np.frexp(exact)[1] - 8, -133).astype(np.float64))  # of a bf16 of this size
+    near = np.where(np.isfinite(exact), np.rint(exact / step) * step, exact)
+    return torch.from_numpy(np.where(np.abs(near) >= 2.0 ** 128, np.copysign(np.inf, near), near)).float().to(torch.bfloat16)
+
+
+def scales_that_tie():
+    """fp32 scales of which some bf16 weight makes a product that fp32 rounds
+    to the middle of two bf16, from where the next rounding goes the wrong way."""
+    rng = np.random.default_rng(12)
+    m = rng.integers(1 << 23, 1 << 24, 60000)
+    low = m[:, None] * np.arange(128, 256)  # 32 bits: of those, fp32 keeps 24 and bf16 8
+    drop = np.where(low >> 31, 8, 7)
+    up = (low + (1 << (drop - 1)) - 1 + (low >> drop & 1)) >> drop  # rounded to 24 bits, ties to even
+    wrong = np.where(up >> 16 & 1, (up << drop) > low, (up << drop) < low)
+    hits = m[(((up & 0xFFFF) == 0x8000) & wrong).any(1)]
+    assert len(hits) > 40
+    return [float(np.float32(v * 2.0 ** -e)) for v, e in zip(hits[:40], [23, 20, 24, 30, 17] * 8)]
+
+
+def test_a_scaled_row_is_rounded_once():
+    """Every bf16 pattern times scales of 24 bits, among them products that
+    land next to a tie, below the normal range and past the largest bf16."""
+    u = (np.arange(65536, dtype=np.int64) * 40503 % 65536).astype(np.uint16)
+    one = table(64 * 1024, "single")
+    ids, few = torch.arange(64, device="cuda"), torch.arange(63, -1, -2, device="cuda")
+    cases = [(u, dim, coded(u)) for dim in (1024, 1000)] + [(one, dim, coded(one)) for dim in (1024, 999)]
+    w = torch.from_numpy(u.view(np.int16)).view(torch.bfloat16)
+    assert len(set(w.view(torch.int16).tolist())) == 65536
+    for scale in scales_that_tie() + [0.1, -1 / 3, float(np.float32(1e-38) * 3), float(np.float32(2.0 ** 127 * 1.2345678)), 1e-45]:
+        for v, dim, dl in cases:
+            rows = v.size // dim
+            t = torch.from_numpy(v.view(np.int16)).view(torch.bfloat16)[: rows * dim].view(rows, dim)
+            want = once(t.double().numpy() * np.float64(np.float32(scale)))
+            at = ids[:rows]
+            for got, sel in ((dfw.embed_rows(t.cuda(), at, scale=scale), at), (dfw.embed_lanes(dl, at, dim, scale=scale), at),
+                             (dfw.embed_lanes(dl, few, dim, scale=scale), few)):
+                assert same(got, want[sel.cpu()]), (scale, dim)
