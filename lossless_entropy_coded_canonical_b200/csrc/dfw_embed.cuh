@@ -712,19 +712,6 @@ struct ReduceParams {
     float scale;
 };
 
-template <typename T>
-__device__ __forceinline__ float as_float(T v);
-template <>
-__device__ __forceinline__ float as_float<float>(float v) { return v; }
-template <>
-__device__ __forceinline__ float as_float<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
-template <typename T>
-__device__ __forceinline__ T from_float(float v);
-template <>
-__device__ __forceinline__ float from_float<float>(float v) { return v; }
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
-
 template <typename T, int N>
 struct __align__(sizeof(T) * N) Pack {
     T v[N];
@@ -753,6 +740,22 @@ struct Raw<__nv_bfloat16, 8> {
     }
 };
 
+// scale x sum (+ what is there), rounded once.  For a bf16 that is the exact
+// value cut to fp32 with a sticky lowest bit, as in mul_odd, then rounded.
+template <typename OUT>
+__device__ __forceinline__ OUT scaled_sum(float scale, float sum, bool add, OUT old);
+template <>
+__device__ __forceinline__ float scaled_sum<float>(float scale, float sum, bool add, float old) {
+    return add ? fmaf(scale, sum, old) : scale * sum;
+}
+template <>
+__device__ __forceinline__ __nv_bfloat16 scaled_sum<__nv_bfloat16>(float scale, float sum, bool add, __nv_bfloat16 old) {
+    if (!add) return __float2bfloat16_rn(mul_odd(scale, sum));
+    const float o = __bfloat162float(old), down = __fmaf_rd(scale, sum, o), up = __fmaf_ru(scale, sum, o);
+    const float z = down >= 0.f ? down : up;  // towards zero
+    return __float2bfloat16_rn(down == up ? up : __uint_as_float(__float_as_uint(z) | 1u));
+}
+
 // Writes (or adds) scale x sum to VEC columns of a row, rounded once; `size` is
 // the gradient's, for the checks build.
 template <typename OUT, int VEC>
@@ -765,7 +768,7 @@ __device__ __forceinline__ void put_row(void *grad, uint64_t at, const float (&a
         Pack<OUT, N> o;
         if (add) o = *dst;
 #pragma unroll
-        for (int j = 0; j < N; ++j) o.v[j] = from_float<OUT>(add ? fmaf(scale, acc[i + j], as_float<OUT>(o.v[j])) : scale * acc[i + j]);
+        for (int j = 0; j < N; ++j) o.v[j] = scaled_sum<OUT>(scale, acc[i + j], add, o.v[j]);
         *dst = o;
     }
 }
@@ -963,7 +966,7 @@ __global__ void __launch_bounds__(256) grad_few(const FewParams p) {
         constexpr int N = VEC * sizeof(OUT) > 16 ? 16 / sizeof(OUT) : VEC;
         Pack<OUT, N> z;
 #pragma unroll
-        for (int j = 0; j < N; ++j) z.v[j] = from_float<OUT>(0.f);
+        for (int j = 0; j < N; ++j) z.v[j] = OUT(0.f);
         OUT *dst = static_cast<OUT *>(p.grad) + r0 * p.dim + col;
         for (uint64_t r = r0; r < r1; ++r, dst += p.dim) {
 #pragma unroll

@@ -6,8 +6,9 @@ fp32 product of a scale of at most 16 bits and a bf16 weight is exact, that of
 a scale of more bits is exact in 64 bits.
 The gradient is a sum of k terms in fp32, in some order: off by at most
 (k + 1) 2^-24 times the scaled sum of magnitudes (one rounding per addition
-and one for the scale), plus 2^-8 of the value for a bf16 result.  Whole
-numbers leave nothing to round.
+and one for the scale), plus 2^-8 of the value for a bf16 result, and exactly
+rounded once where the sum itself is exact.  Whole numbers leave nothing to
+round.
 """
 from __future__ import annotations
 
@@ -571,3 +572,54 @@ def test_a_scaled_row_is_rounded_once():
             for got, sel in ((dfw.embed_rows(t.cuda(), at, scale=scale), at), (dfw.embed_lanes(dl, at, dim, scale=scale), at),
                              (dfw.embed_lanes(dl, few, dim, scale=scale), few)):
                 assert same(got, want[sel.cpu()]), (scale, dim)
+
+
+def values_that_tie(scale, base):
+    """fp32 values v (and bf16 numbers o to add to them, 0 without base) whose
+    scale v + o, exact in 64 bits, misses its nearest bf16 by way of fp32."""
+    rng = np.random.default_rng(21)
+    v = rng.integers(-(1 << 24), 1 << 24, 12_000_000).astype(np.float64)  # scale v: 48 bits
+    o = torch.from_numpy(rng.integers(-(1 << 47), 1 << 47, v.size)).double().float().to(torch.bfloat16).double().numpy() if base else 0 * v
+    exact = scale * v + o
+    hit = once(exact).view(torch.int16) != torch.from_numpy(exact.astype(np.float32)).to(torch.bfloat16).view(torch.int16)
+    hit = hit.numpy()
+    assert hit.sum() > 40
+    return v[hit], o[hit]
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("rows,dim,each", [(60, 40, 1), (2, 33, 40), (2000, 24, 1), (900, 17, 7), (40, 64, 60), (3, 31, 900), (2, 72, 700)])
+def test_a_bf16_gradient_is_rounded_once(rows, dim, each, accumulate):
+    """Rows of one token that counts, the others' gradients being zero: the
+    sum is exact, and scale x sum (+ the old value) is rounded once.  Few
+    tokens, rows inside a window, over a few windows and over many."""
+    scale = float((1 << 23) + 5_000_001)
+    v, o = values_that_tie(scale, accumulate)
+    at = np.arange(rows * dim) % v.size
+    rng = np.random.default_rng(each)
+    ids = rng.permutation(np.repeat(np.arange(rows), each))
+    dy = np.zeros((ids.size, dim), dtype=np.float32)
+    counts = np.array([rng.choice(np.nonzero(ids == r)[0]) for r in range(rows)])
+    dy[counts] = v[at].reshape(rows, dim)
+    old = torch.from_numpy(o[at].reshape(rows, dim)).float().to(torch.bfloat16).cuda()
+    want = once(scale * v[at] + o[at]).view(rows, dim)
+    got = dfw.embed_grad(torch.from_numpy(ids).cuda(), torch.from_numpy(dy).cuda(), rows, scale=scale, out=old, accumulate=accumulate)
+    assert torch.equal(got.cpu(), want)
+
+
+def test_a_bf16_gradient_at_the_ends_of_the_range():
+    """Zeros, infinities, NaN, results past the largest bf16 and below the normal range."""
+    ids = torch.arange(12, device="cuda", dtype=torch.int32)
+    big, tiny = 3.3e38, 2.0 ** -120
+    dy = torch.tensor([0.0, 2.0, float("inf"), -float("inf"), float("nan"), big, -big, tiny, -tiny, 1e-45, 1.0, -1.0], device="cuda")
+    dy = dy[:, None].expand(12, 8).contiguous()
+    for scale in (1.0, 1.1, -3.7, 1e-12, 1e30):
+        s = np.float64(np.float32(scale))
+        exact = dy.double().cpu().numpy() * s
+        assert same(dfw.embed_grad(ids, dy, 12, scale=scale, out_dtype=torch.bfloat16), once(exact))
+        for old in (0.0, -2.0 ** -133, 2.0 ** 127, -float("inf")):
+            out = torch.full((12, 8), old, dtype=torch.bfloat16, device="cuda")
+            with np.errstate(invalid="ignore"):  # infinities of both signs
+                want = once(exact + float(out[0, 0]))
+            dfw.embed_grad(ids, dy, 12, scale=scale, out=out, accumulate=True)
+            assert same(out, want), (scale, old)
