@@ -623,3 +623,41 @@ def test_a_bf16_gradient_at_the_ends_of_the_range():
                 want = once(exact + float(out[0, 0]))
             dfw.embed_grad(ids, dy, 12, scale=scale, out=out, accumulate=True)
             assert same(out, want), (scale, old)
+
+
+@pytest.fixture(scope="module")
+def long_groups():
+    """A scope of 2.15e6 weights whose rare exponents lie together: two groups
+    of codewords of 17 bits among groups of 2, (patterns, first of the rare
+    weights, scope)."""
+    rng = np.random.default_rng(17)
+    rare = rng.permutation(np.repeat(np.arange(200), 21))
+    chain = rng.permutation(np.repeat(200 + np.arange(9), 4200 << np.arange(9)))
+    at = 1_000_003
+    e = np.concatenate([chain[:at], rare, chain[at:]]) + 20
+    u = ((rng.integers(0, 2, e.size) << 15) | (e << 7) | rng.integers(0, 128, e.size)).astype(np.uint16)
+    return u, at, coded(u)
+
+
+@pytest.mark.parametrize("dim,first", [(1024, 0), (2048, 2048), (4096, 16), (1000, 8), (6000, 0), (777, 5), (3001, 0)])
+@pytest.mark.parametrize("tokens", [1, 9, 2000])
+def test_coded_rows_of_long_codewords(long_groups, dim, first, tokens):
+    """Slots so long that not even 16 warps of them fit an SM with the table:
+    the smallest CTAs, of one warp, looking up the long groups and others."""
+    u, at, dl = long_groups
+    slot = int(dl.info.max_group_bytes)
+    warp = 32 + 2 * (64 + slot) + 2048 + 17 * 136 + 8  # barriers, two slots, raw bytes, exponents (a multiple of 16)
+    assert (8 << int(dl.info.fast_bits)) + 16 * warp > 227 * 1024
+    rows = (u.size - first) // dim
+    mid = (at - first) // dim
+    rng = np.random.default_rng(dim)
+    ids = np.where(rng.random(tokens) < 0.5, mid + rng.integers(0, 4200 // dim + 2, tokens), rng.integers(0, rows, tokens))
+    ids[:4] = (mid, rows - 1, -1, 0)[:tokens]
+    ids = torch.from_numpy(ids)
+    want = rows_of(u, first, rows, dim, ids, 1.0)
+    assert torch.equal(dfw.embed_lanes(dl, ids.cuda(), dim, first=first).cpu().view(torch.int16), want.view(torch.int16))
+    for scale in (-45.25, 0.1):
+        exact = torch.from_numpy(u.view(np.int16)).view(torch.bfloat16)[first: first + rows * dim].view(rows, dim)[ids.clamp(min=0)].double().numpy()
+        exact[(ids < 0).numpy()] = 0.0
+        got = dfw.embed_lanes(dl, ids.cuda(), dim, scale=scale, first=first)
+        assert torch.equal(got.cpu(), once(exact * np.float64(np.float32(scale))))
