@@ -637,6 +637,7 @@ def q4_quantise(w: torch.Tensor, group: int = 128, zeros: bool = False, stream=N
 
 def q4_dequantise(q: Q4Weights, stream=None) -> torch.Tensor:
     """The bf16 matrix [rows, cols] that ``q`` stands for (``dfw_q4_dequantise``)."""
+    _expect("packed", q.packed, q.packed.device, _BYTES)
     sh = _here(q.packed.device, stream)
     if sh is None:
         with _there(q.packed.device, stream):

@@ -159,3 +159,12 @@ def test_packed_weights_must_be_what_their_info_says():
     for packed in (whole, whole[:info.bytes - 1], whole[:info.bytes].view(torch.int8), torch.zeros(info.bytes * 2, dtype=torch.uint8)[::2]):
         with pytest.raises(ValueError):
             dfw.Q4Weights(packed, info)
+
+
+def test_binding_refuses_packed_weights_on_the_host():
+    """Packed weights may lie on the host (read from a file, say): not for these calls."""
+    info = q4_info(16, 128, 128)
+    q = dfw.Q4Weights(torch.zeros(info.bytes, dtype=torch.uint8), info)
+    for call in (lambda: dfw.q4_dequantise(q), lambda: dfw.q4_gemv(q, torch.zeros(1, 128, dtype=torch.bfloat16))):
+        with pytest.raises(ValueError, match="must be on a CUDA device"):
+            call()
