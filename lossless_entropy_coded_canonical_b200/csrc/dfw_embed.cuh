@@ -433,6 +433,8 @@ __device__ __forceinline__ void single_row(const RowScale &s, const uint8_t *m, 
 
 template <int V>
 __global__ void __launch_bounds__(256) embed_single_rows(const RowsOfLanes p) {
+    griddep_wait();
+    griddep_launch_dependents();
     const uint32_t E = rot_sym(p.single) * 0x01010101u, lane = threadIdx.x & 31u;
     for (uint32_t t = blockIdx.x * 8u + (threadIdx.x >> 5); t < p.ids.tokens; t += gridDim.x * 8u) {
         uint64_t row = 0;
@@ -1125,7 +1127,7 @@ dfw_status launch_embed_lanes(const dfw_lanes_scope *scope, uint64_t first, uint
         const uint64_t want = (tokens + 7u) / 8u;
         const bool vec = out16 && first % 8u == 0u && dim % 8u == 0u;
         return launch_with(vec ? embed_single_rows<8> : embed_single_rows<1>, std::min<uint64_t>(want, (uint64_t)sms * 8u), 256, 0,
-                           false, 1, s, p);
+                           true, 1, s, p);
     }
     const bool whole = first % GROUP_SYMS == 0u && (dim % GROUP_SYMS == 0u || GROUP_SYMS % dim == 0u);
     p.units = (dim + GROUP_SYMS - (whole ? 1u : 2u)) / GROUP_SYMS + (whole ? 0u : 1u);

@@ -661,3 +661,25 @@ def test_coded_rows_of_long_codewords(long_groups, dim, first, tokens):
         exact[(ids < 0).numpy()] = 0.0
         got = dfw.embed_lanes(dl, ids.cuda(), dim, scale=scale, first=first)
         assert torch.equal(got.cpu(), once(exact * np.float64(np.float32(scale))))
+
+
+def test_rows_of_one_exponent_between_other_calls():
+    """Lookups in a scope of one exponent that follow each other and other
+    calls without a gap: each reads ids, or writes rows, that the calls around
+    it write or read."""
+    rows, dim, tokens = 4000, 1024, 6000
+    one, u = table(rows * dim, "single", 3), table(rows * dim, seed=4)
+    a, b = coded(one), coded(u)
+    assert int(a.table.total_bits) == 0
+    lists = [ids_for(rows, tokens, 10 + i).cuda() for i in range(3)]
+    want = [[rows_of(v, 0, rows, dim, i.cpu(), 2.0).cuda() for i in lists] for v in (one, u)]
+    ids, x = torch.empty_like(lists[0]), torch.empty(tokens, dim, dtype=torch.bfloat16, device="cuda")
+    for step in range(12):
+        kept = []
+        for i in lists:
+            ids.copy_(i)
+            for dl in (a, a, b, a):
+                dfw.embed_lanes(dl, ids, dim, scale=2.0, out=x)
+                kept.append(dfw.embed_rows(x, torch.arange(0, tokens, 50, device="cuda")))
+        for n, got in enumerate(kept):
+            assert torch.equal(got, want[1 if n % 4 == 2 else 0][n // 4][::50]), (step, n)
