@@ -160,12 +160,11 @@ struct RowsOfLanes {
     IdSource ids;
     LanesParams lanes;     // the scope (out unused)
     uint64_t first;        // the table's first weight in the scope
-    uint64_t total_bits;
     uint16_t *out;
     uint64_t ldo;
     uint32_t dim;
     uint32_t units;        // the most groups a row meets
-    uint32_t single;       // total_bits == 0: every exponent is this one
+    uint32_t single;       // embed_single_rows: every exponent is this one
     RowScale scale;
 };
 
@@ -828,7 +827,7 @@ __global__ void __launch_bounds__(128, 6) grad_reduce(const ReduceParams p) {
         if (cur >= p.rows) return;
         const bool left = first && cur == prev, right = last && cur == next;
         if (left || right) {
-            if (!check(p.windows > 1u && w < p.windows && col + VEC <= p.dim, CK_GRAD_PARTIAL)) return;
+            if (!check(w < p.windows && col + VEC <= p.dim, CK_GRAD_PARTIAL)) return;
             float *dst = p.partial + ((uint64_t)w * 2u + (left ? 0u : 1u)) * p.dim + col;
             constexpr int N = VEC > 4 ? 4 : VEC;
 #pragma unroll
@@ -1115,7 +1114,6 @@ dfw_status launch_embed_lanes(const dfw_lanes_scope *scope, uint64_t first, uint
     if ((st = device_sms(sms)) != DFW_OK) return st;
     p.lanes.mant = scope->d_mant;
     p.first = first;
-    p.total_bits = table->total_bits;
     p.out = d_out;
     p.ldo = ld_out;
     p.dim = dim;
@@ -1136,8 +1134,11 @@ dfw_status launch_embed_lanes(const dfw_lanes_scope *scope, uint64_t first, uint
     return launch_embed_width<1>(p, sms, s);
 }
 
-// How the gradient of `tokens` tokens is cut: blocks of `block` tokens that a
-// cluster sorts, windows for summing.
+// How the gradient of more than GRAD_FEW tokens is cut: blocks of `block`
+// tokens that a cluster sorts, windows of at most GRAD_WINDOW for summing.  The
+// cut is the same on every device (it fixes the order of the sums and the
+// size of the scratch), made for 148 SMs.
+constexpr uint32_t GRAD_WINDOW = 128;
 struct GradCut {
     uint32_t ctas, ipt, block, blocks, window, windows;
     uint32_t joins;  // bytes of the joins lists
@@ -1159,7 +1160,8 @@ GradCut grad_cut(uint64_t tokens, uint32_t dim) {
     while (threads < 128u && threads * 8u < dim) threads *= 2u;
     threads *= (dim + 8u * threads - 1u) / (8u * threads);
     const uint64_t window = (tokens * threads + 128u * 888u - 1u) / (128u * 888u);
-    c.window = (uint32_t)std::min<uint64_t>(128u, std::max<uint64_t>(tokens <= 1024u ? 8u : tokens <= 16384u ? 16u : 64u, (window + 7u) & ~7ull));
+    static_assert(GRAD_WINDOW <= GRAD_FEW, "at least two windows: there is always something that may have to be joined");
+    c.window = (uint32_t)std::min<uint64_t>(GRAD_WINDOW, std::max<uint64_t>(tokens <= 1024u ? 8u : tokens <= 16384u ? 16u : 64u, (window + 7u) & ~7ull));
     c.windows = (uint32_t)((tokens + c.window - 1u) / c.window);
     c.list = (tokens * 4u + 15u) & ~15ull;
     c.joins = ((4u + 2u * c.windows) * 4u + 15u) & ~15u;
@@ -1169,7 +1171,7 @@ GradCut grad_cut(uint64_t tokens, uint32_t dim) {
 uint64_t embed_grad_scratch(uint64_t tokens, uint32_t dim) {
     if (tokens <= GRAD_FEW) return 0u;
     const GradCut c = grad_cut(tokens, dim);
-    return c.joins + c.list * (c.blocks > 1u ? 4u : 2u) + (c.windows > 1u ? (uint64_t)c.windows * 2u * dim * 4u : 0u);
+    return c.joins + c.list * (c.blocks > 1u ? 4u : 2u) + (uint64_t)c.windows * 2u * dim * 4u;
 }
 
 template <int C, int IPT, bool PACK>
@@ -1204,7 +1206,7 @@ dfw_status launch_grad_reduce(ReduceParams p, int sms, cudaStream_t s) {
     const uint64_t per = 128u / p.tpr;
     dfw_status st = launch_with(grad_reduce<DY, OUT, V>, (p.windows + per - 1u) / per * p.col_blocks, 128, per * p.window * 8u,
                                 true, 1, s, p);
-    if (st != DFW_OK || p.windows < 2u) return st;
+    if (st != DFW_OK) return st;
     constexpr uint32_t J = V > 4 ? 4 : V;
     const uint64_t most = (uint64_t)(p.windows - 1u) * ((p.dim + 32u * J - 1u) / (32u * J));
     return launch_with(grad_join<OUT, (int)J>, std::min<uint64_t>(most, (uint64_t)sms * 8u), 256, 0, true, 1, s, p);
