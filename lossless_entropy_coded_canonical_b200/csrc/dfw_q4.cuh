@@ -289,7 +289,9 @@ __global__ void __launch_bounds__(256) q4_dequantise_tiles(const uint8_t *__rest
 // left room for half the warps).  A warp leaves its sums of each row tile it
 // touched in shared memory; at the end of the pass they are added in the
 // warps' order.  When the vectors are too long for one SM's shared memory, a
-// cluster of 2 to 8 CTAs shares the columns and joins its sums the same way.
+// cluster of 2 to 8 CTAs shares the columns and joins its sums the same way
+// (no CTA of it is without column tiles: vectors that long have 34 of them for
+// 2 CTAs, 59 for 4, 117 for 8).
 // Up to 8 vectors take 32 warps of 64 registers, or 16 where their shared
 // memory does not allow 32 or the CTA has few tiles; 9 to 16 have twice the
 // sums and take 16.
@@ -454,7 +456,7 @@ __global__ void __launch_bounds__(32 * W, 1) q4_gemv_tiles(const Q4GemvParams a)
     const uint32_t outs = 16u * a.m;  // sums of a row tile, column by column
     const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3u;
     const uint32_t split = SPLIT ? a.split : 1u, rank = blockIdx.x % split, me = blockIdx.x / split;
-    const uint32_t ct0 = rank * a.tiles, cts = ct0 < a.q.col_tiles ? min(a.tiles, a.q.col_tiles - ct0) : 0u;
+    const uint32_t ct0 = rank * a.tiles, cts = min(a.tiles, a.q.col_tiles - ct0);
     const uint32_t rt0 = me * a.share + min(me, a.extra), rows = a.share + (me < a.extra ? 1u : 0u);  // row tiles
     const uint32_t ring = smem_u32(smem) + warp * RING * SLOT + 16u * lane;  // a lane's own place in it
     float *sums = reinterpret_cast<float *>(smem + W * RING * SLOT);
@@ -477,7 +479,7 @@ __global__ void __launch_bounds__(32 * W, 1) q4_gemv_tiles(const Q4GemvParams a)
                      CK_Q4_COPY);
     };
     auto fetch = [&]() {
-        while (in_left == 0u && in_row < rows && cts) {  // the next pass
+        while (in_left == 0u && in_row < rows) {  // the next pass
             const uint32_t n = min(a.pass, rows - in_row), lo = first(warp, n);
             in_left = first(warp + 1u, n) - lo;
             in_ct = lo % cts;
@@ -522,7 +524,7 @@ __global__ void __launch_bounds__(32 * W, 1) q4_gemv_tiles(const Q4GemvParams a)
     if (v < a.m) {
         const uint16_t *x = a.x + v * a.ldx + Q4_COLS * ct0;
         uint8_t *dst = vecs + v * a.pitch;
-        const uint32_t here = (min(a.q.cols, Q4_COLS * (ct0 + cts)) - min(a.q.cols, Q4_COLS * ct0)) / 8u;
+        const uint32_t here = (min(a.q.cols, Q4_COLS * (ct0 + cts)) - Q4_COLS * ct0) / 8u;
         for (uint32_t c = threadIdx.x & ((1u << log) - 1u); c < 16u * cts; c += 1u << log) {
             if (c >= here) {
                 *reinterpret_cast<uint4 *>(dst + 16u * c) = make_uint4(0u, 0u, 0u, 0u);
@@ -562,7 +564,7 @@ __global__ void __launch_bounds__(32 * W, 1) q4_gemv_tiles(const Q4GemvParams a)
 
     for (uint32_t done = 0; done < rows; done += a.pass) {
         const uint32_t n = min(a.pass, rows - done), lo = first(warp, n), hi = first(warp + 1u, n);
-        uint32_t row = cts ? lo / cts : 0u, ct = lo - row * cts;
+        uint32_t row = lo / cts, ct = lo - row * cts;
         for (uint32_t i = lo; i < hi; i += Q4_STEP) {
             cp_async_wait<(int)RING - 2>();
             __syncwarp();  // every lane's copies, and every lane is done with the slot that fetch() fills
@@ -583,19 +585,17 @@ __global__ void __launch_bounds__(32 * W, 1) q4_gemv_tiles(const Q4GemvParams a)
         __syncthreads();
         // row tile r's sums: those of the warps whose runs meet tiles [r cts,
         // (r + 1) cts), from the first that ends behind r cts
-        const uint32_t tiles = n * cts, inv = cts ? 0xFFFFFFFFu / tiles : 0u;
+        const uint32_t tiles = n * cts, inv = 0xFFFFFFFFu / tiles;
         auto quotient = [&](uint32_t x) {  // x / tiles (x below 2^25: the estimate is at most one short)
             const uint32_t q = __umulhi(x, inv);
             return (q + 1u) * tiles <= x ? q + 1u : q;
         };
         for (uint32_t i = threadIdx.x; i < n * outs; i += 32u * W) {
             const uint32_t r = __umulhi(i, a.outs_inv), o = i - r * outs;
+            const uint32_t w0 = quotient((r * cts + 1u) * W + tiles - 1u) - 1u, w1 = quotient((r + 1u) * cts * W + tiles - 1u);
             float v = 0.f;
-            if (cts) {
-                const uint32_t w0 = quotient((r * cts + 1u) * W + tiles - 1u) - 1u, w1 = quotient((r + 1u) * cts * W + tiles - 1u);
 #pragma unroll 8
-                for (uint32_t w = w0; w < w1; ++w) v += sums[(w + r) * outs + o];
-            }
+            for (uint32_t w = w0; w < w1; ++w) v += sums[(w + r) * outs + o];
             if constexpr (!SPLIT) {
                 q4_store(a, (uint64_t)Q4_ROWS * (rt0 + done + r) + (o & 15u), o >> 4, v);
             } else {
