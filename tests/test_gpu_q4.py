@@ -328,3 +328,19 @@ def test_offsets_past_32_bits():
     codes[-1, -1], scales[-1, -1] = 0xF8, 2.0
     y = dfw.q4_gemv(dfw.q4_pack(codes, scales), torch.ones(cols, dtype=torch.bfloat16, device="cuda"))
     assert y[-1] == 14.0 and not y[:-1].any()
+
+
+@pytest.mark.parametrize("x_exp,s_exp", [(-130, 100), (-133, 120), (100, -110), (-60, -50), (0, -118), (120, 0), (-126, 127)])
+def test_vectors_and_scales_far_from_one(x_exp, s_exp):
+    """Whole numbers times powers of two, vectors below the normal range among
+    them: exact as long as no result is below 2^-120 (the sums are kept over
+    64), infinite where the result, not a sum on the way, is past fp32."""
+    rows, cols, group = 70, 640, 64
+    q, s, z = make(rows, cols, group, True, 31)
+    s = np.full(s.shape, 2.0 ** s_exp)
+    for tokens in (1, 12):
+        x = vectors(tokens, cols, 5, whole=True)
+        with np.errstate(over="ignore"):
+            want = (x.double().numpy() @ weights(q, s, z, group).T * 2.0 ** x_exp).astype(np.float32)
+        y = dfw.q4_gemv(to_gpu(q, s, z, group), (x.double() * 2.0 ** x_exp).to(torch.bfloat16).cuda())
+        assert np.array_equal(y.cpu().numpy(), want)
