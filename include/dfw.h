@@ -726,12 +726,15 @@ dfw_status dfw_q4_dequantise(const uint8_t *d_packed, const dfw_q4_info *info, u
  *   d_y    device, result j at element j ldy (ldy >= rows for m > 1): fp32
  *          if y_fp32 is 1, else bf16
  * Arithmetic: (q - z) and x are exact in bf16 and their products exact; a
- * group's products are summed in fp32, the sums multiplied by their scales
- * and added in fp32, in an order fixed by the shape (repeated calls give
- * identical bits); a bf16 result is rounded once.  More than 16 vectors (8 or
- * 4 for more than 24576 or 32768 columns) read the weights again for every 16.
- * d_y must not overlap an input.  Asynchronous; needs no scratch.  Errors: DFW_EINVAL, DFW_EALIGN (d_packed 16 bytes, d_x and d_y
- * their element), DFW_ECUDA.
+ * group's products are summed by matrix instructions, which add 16 of them to
+ * an fp32 sum at a time and may cut each at 2^-23 of the largest; the sums are
+ * multiplied by their scales and added in fp32, in an order fixed by the shape
+ * (repeated calls give identical bits); a bf16 result is rounded once.  All of
+ * it is 1/64 of the result until the end, so results below 2^-120 lose bits.
+ * More than 16 vectors (8 or 4 for more than 24576 or 32768 columns) read the
+ * weights again for every 16 (8 or 4).  d_y must not overlap an input.
+ * Asynchronous; needs no scratch.  Errors: DFW_EINVAL, DFW_EALIGN (d_packed 16
+ * bytes, d_x and d_y their element), DFW_ECUDA.
  */
 dfw_status dfw_q4_gemv(const uint8_t *d_packed, const dfw_q4_info *info, uint32_t m, const uint16_t *d_x,
                        uint64_t ldx, void *d_y, int y_fp32, uint64_t ldy, void *cuda_stream);
@@ -745,8 +748,9 @@ dfw_status dfw_q4_gemv(const uint8_t *d_packed, const dfw_q4_info *info, uint32_
  * ids64 = 1.  Asynchronous.
  *
  * dfw_embed_lanes -- the table is entropy-coded: weights [first, first + rows
- * dim) of a scope with its known-start plan (the chunks a row needs are
- * decoded, nothing else is read; a row may start anywhere in a chunk).
+ * dim) of a scope with its known-start plan (a row may start anywhere in a
+ * chunk).  The groups of 2048 weights that a row meets are read whole, also for
+ * a row of a few weights; of them the chunks that the row needs are decoded.
  * Source: DFloat11 abstract point (iii), decompression of a part of the
  * model on demand; the LazyWeights write-up (lanes with known starts).
  *   scope    as for dfw_decode_lanes_seq; a group found corrupt writes
@@ -755,8 +759,9 @@ dfw_status dfw_q4_gemv(const uint8_t *d_packed, const dfw_q4_info *info, uint32_
  * dfw_embed_rows -- the table is bf16 (a decoded scope): row v at
  * d_table + v ld_table (ld_table >= dim).
  * d_out must not overlap an input.  Limits: tokens <= DFW_EMBED_MAX_TOKENS,
- * rows <= DFW_EMBED_MAX_ROWS, dim <= DFW_EMBED_MAX_DIM.  Errors: DFW_EINVAL, DFW_EALIGN (ids and bf16 pointers
- * to their element, the scope's buffers as dfw_decode_lanes), DFW_ECUDA.
+ * rows <= DFW_EMBED_MAX_ROWS, dim <= DFW_EMBED_MAX_DIM.  Errors: DFW_EINVAL,
+ * DFW_EALIGN (ids and bf16 pointers to their element, the scope's buffers as
+ * dfw_decode_lanes), DFW_ECUDA.
  */
 #define DFW_EMBED_MAX_TOKENS 1048576u
 #define DFW_EMBED_MAX_ROWS 1073741824u
@@ -775,8 +780,9 @@ dfw_status dfw_embed_rows(const uint16_t *d_table, uint64_t rows, uint32_t dim, 
  * sum of dy[t, :] over the tokens t with id v.  Padding ids and ids past the
  * table (reported through dfw_check) are left out.  Sums are fp32, their
  * order fixed by the ids and the shape (the tokens are sorted by id, a row's
- * tokens stay in order), so repeated calls give identical bits.  The result
- * can update a decoded table, which dfw_encode_device codes again.
+ * tokens stay in order), so repeated calls give identical bits; scale x sum is
+ * rounded once, to fp32 or bf16.  The result can update a decoded table, which
+ * dfw_encode_device codes again.
  *   d_dy        device, fp32 if dy_fp32 is 1, else bf16; row t at t ld_dy
  *   d_grad      device, rows x dim, contiguous, fp32 if grad_fp32 is 1, else
  *               bf16.  accumulate 0: every row is written (zeros where no

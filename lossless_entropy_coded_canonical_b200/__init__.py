@@ -706,10 +706,11 @@ def _rows_contiguous(t: torch.Tensor) -> bool:
 def embed_lanes(dl: DeviceLanes, ids: torch.Tensor, dim: int, scale: float = 1.0, first: int = 0,
                 rows: int | None = None, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Rows of an entropy-coded embedding table by token id, scaled
-    (``dfw_embed_lanes``): only the chunks those rows need are decoded.  The
-    table is weights [first, first + rows dim) of the scope (by default all
-    whole rows from ``first``).  ``ids``: int32 or int64, any shape, negative =
-    padding (a zero row); returns bf16 [*ids.shape, dim]."""
+    (``dfw_embed_lanes``): only those rows' groups are read, only their chunks
+    decoded.  The table is weights [first, first + rows dim) of the scope (by
+    default all whole rows from ``first``).  ``ids``: int32 or int64, any
+    shape, contiguous, negative = padding (a zero row); returns bf16
+    [*ids.shape, dim]."""
     dev = dl.mant.device
     sh = _here(dev, stream) if dl.mant.is_cuda else 0
     if sh is None:

@@ -48,11 +48,11 @@ __device__ __forceinline__ bool token_row(const IdSource &s, uint32_t t, uint64_
 // tie of a bf16 only if the exact one is, so the conversion to bf16 is the only
 // rounding.  (From the nearest fp32, a value beside a tie could land on it: for
 // some scales 1 in 130 weights went the wrong way.)  The neighbours' bits are
-// consecutive numbers, so one of them is odd.  It costs little: 8192 bf16
-// gradient rows of 4096 take 71.0 us against 70.0, 45.6 against 42.1 if they are
-// added to the old ones, as many coded rows with such a scale 33 against 31.
-// (Working only those out again whose fp32 value is a tie: 75 to 79 us, as the
-// second copy of the arithmetic takes registers from the rows in flight.)
+// consecutive numbers, so one of them is odd.  It costs little: a bf16 gradient
+// of 8192 rows of 4096 takes 71.0 us against 70.0, 45.6 against 42.1 if it is
+// added to the old values, as many coded rows with such a scale 32 to 33
+// against 31.  (Working out again only what is a tie in fp32: 75 to 79 us, as
+// the second copy of the arithmetic takes registers from the rows in flight.)
 __device__ __forceinline__ float mul_odd(float a, float b) {
     return __uint_as_float(__float_as_uint(__fmul_rz(a, b)) | (__float_as_uint(__fmul_ru(fabsf(a), fabsf(b))) & 1u));
 }
@@ -213,17 +213,19 @@ __device__ __forceinline__ void join_row(const RowScale &s, uint16_t *out, uint3
 // row (the first ones of all tokens, then the second ones; rows that begin
 // anywhere meet fewer groups than others, and those units are passed over),
 // staged as decode_lanes stages its own (the same copies, positions, lookups
-// and checks), except that lanes whose chunk the row does not touch decode
-// nothing, and the join scales and writes the row's part of the group.  (Rows
-// that are not whole groups as one unit each: 3 rows of 20000 32 us, so 7; 67
-// of 5365 17.7 and 8.5; 2000 of 5365 27 and 24; 8000 of 1000 21.6 and 21.5;
-// 4000 of 1001 15.4 and 17.)
+// and checks: a group is read whole), except that lanes whose chunk the row
+// does not touch decode nothing, and the join scales and writes the row's part
+// of the group.  (Rows that are not whole groups as one unit each: 3 rows of
+// 20000 32 us, so 7; 67 of 5365 17.7 and 8.3; 2000 of 5365 27 and 23; 8000 of
+// 1000 21.6 and 21.3; 4000 of 1001 15.4 and 16.8.)
 // The starts of the group after the current one are loaded ahead; the table's
 // copy and check overlap the first group's three dependent loads (id, group
 // start, stream).
-// Bound by instruction issue, as the decode: 8192 rows of 4096 take 29.3 us,
-// 0.18 per group and SM past 10 of start (32 us with a unit's id loaded by
-// itself); one row 6.1, a chain of dependent loads.
+// 8192 rows of 4096 take 29.3 us, 0.18 per group and SM past 10 of start (32 us
+// with a unit's id loaded by itself): 1245 warp instructions per group (the
+// decode's 1011), 64% of the issue slots, 55% of the integer pipe.  One row 6.1,
+// a chain of dependent loads.  Rows narrower than a group cost a group each:
+// 16384 rows of 192 24.9 us, of 72 23.6.
 // V: the join's weights per access; every row begins at a multiple of V in
 // the scope and at 2 V bytes in the output (V = 1: no alignment).
 template <int NT, int V>
@@ -414,6 +416,8 @@ __global__ void __launch_bounds__(NT) embed_lanes_rows(const RowsOfLanes p) {
 }
 
 // Rows of a scope with one exponent (no stream): raw bytes joined with it.
+// Bound by memory: 8192 rows of 4096 take 14.7 us (6.9 TB/s, repeated rows from
+// L2), one row 2.7.
 template <ScaleKind KIND, int V>
 __device__ __forceinline__ void single_row(const RowScale &s, const uint8_t *m, uint32_t E, uint16_t *out, uint32_t dim, uint32_t lane) {
 #pragma unroll 4
@@ -704,8 +708,9 @@ constexpr uint32_t JOIN_FEW = 8;
 // walks a window with VEC columns, eight rows of dy in flight, and writes a
 // row's sum when the next row's tokens begin.  A row whose tokens reach past
 // the window leaves a partial sum instead (slot 0 if it came from the window
-// before, else slot 1); grad_join adds those up in window order.  Bound by
-// HBM: 8192 rows of 4096 bf16 18.1 us, 65536 of 1024 26.4 (5.1 TB/s).
+// before, else slot 1); grad_join adds those up in window order.  Bound by the
+// loads' latency (20 warps an SM, each waiting for its eight rows): 8192 rows
+// of 4096 bf16 19.7 us, 65536 of 1024 27 (5.0 TB/s).
 struct ReduceParams {
     const uint32_t *keys, *pos;
     const void *dy;
@@ -871,7 +876,7 @@ __global__ void __launch_bounds__(128, 6) grad_reduce(const ReduceParams p) {
 // of them for its VEC columns.  Many (a row that a good part of the tokens
 // share): for 32 VEC columns at a time each warp adds every eighth window,
 // then the eight sums are added in order.  Bound by the latency of three loads
-// in a chain (list, key, sums): 9.0 us after 8192 rows of 4096, 12.8 after
+// in a chain (list, key, sums): 9.2 us after 8192 rows of 4096, 14.3 after
 // 65536 of 1024 into 259 rows.
 template <typename OUT, int VEC>
 __global__ void __launch_bounds__(256) grad_join(const ReduceParams p) {
@@ -1082,7 +1087,10 @@ dfw_status launch_embed_groups(const RowsOfLanes &p, uint32_t smem, int sms, cud
 template <int V>
 dfw_status launch_embed_width(const RowsOfLanes &p, int sms, cudaStream_t s) {
     const uint32_t table = 8u << p.lanes.fast_bits, warp = warp_smem_bytes(p.lanes.sbuf_bytes);
-    // 32 warps per SM; fewer where their slots do not fit (long codewords)
+    // 32 warps per SM; fewer where their slots do not fit (long codewords; the
+    // scope's longest group decides: 2048 weights of 23 bits among 131e6 of 2.6
+    // make 8192 rows of 4096 97 us instead of 29.6, one row 20.8 instead of 6.1,
+    // as every one-warp CTA copies and checks a table of its own)
     if (table + 32u * warp <= SMEM_MOST) return launch_embed_groups<1024, V>(p, table + 32u * warp, sms, s);
     if (table + 16u * warp <= SMEM_MOST) return launch_embed_groups<512, V>(p, table + 16u * warp, sms, s);
     return launch_embed_groups<32, V>(p, table + warp, sms, s);

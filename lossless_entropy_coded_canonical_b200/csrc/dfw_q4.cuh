@@ -125,8 +125,9 @@ __device__ __forceinline__ uint32_t q4_split(uint32_t w) {
 // zero points -> tiles.  One thread per word of codes; the first threads of a
 // tile also place its scales and zero points.  (Here and in the next two a
 // CTA walks tiles of one row tile: dividing a running tile number cost 0.3 to
-// 0.7 ms on 128256 x 4096.)  Bound by HBM: 128256 x 4096
-// takes 142 us, 3.8 TB/s read and written.
+// 0.7 ms on 128256 x 4096.)  Bound by instructions, which fill 70% of the
+// issue slots and 64% of the integer pipe: 128256 x 4096 takes 141 us, 3.8 TB/s
+// read and written.
 __global__ void __launch_bounds__(256) q4_pack_tiles(const uint8_t *__restrict__ codes,
                                                      const uint16_t *__restrict__ scales,
                                                      const uint8_t *__restrict__ zeros, const Q4Params p,
@@ -188,7 +189,8 @@ __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
 // bf16 weights -> tiles.  A thread takes a word's eight columns, sixteen
 // threads a row of a tile, 16 / GT of them a group, whose extremes they find
 // by shuffles.  The codes are those of the formula in include/dfw.h.  Bound by
-// instructions: 128256 x 4096 takes 506 us, 2.6 TB/s read and written, against
+// instructions, which fill 87% of the issue slots: 128256 x 4096 takes 505 us,
+// 2.6 TB/s read and written, against
 // 709 with the extremes of a thread's weights found in fp32 and the choice
 // between product and division made per weight, 1384 with a division per weight.
 __global__ void __launch_bounds__(256) q4_quantise_tiles(const uint16_t *__restrict__ w, uint64_t ldw, uint32_t vec,
@@ -296,13 +298,18 @@ __global__ void __launch_bounds__(256) q4_dequantise_tiles(const uint8_t *__rest
 // memory does not allow 32 or the CTA has few tiles; 9 to 16 have twice the
 // sums and take 16.
 //
-// What bounds it: 128256 x 4096 with 4 vectors takes 48.8 us, 5.6 TB/s of the
+// What bounds it: 128256 x 4096 with 4 vectors takes 48.1 us, 5.7 TB/s of the
 // 6.5 a copy reaches; the same loop takes 46.1 us with neither expansion nor
 // products, so the copies bound it (the shift in the expansion as a
 // multiplication's high half, meant to spare the integer pipe, made that
-// 54.5).  Small matrices are bound by the chain of a launch, the first copies
-// and the join: 1024 x 4096, one vector, 3.7 us, of which a launch of one tile
-// takes 2.7; 6144 x 4096 7.2 us, 6.2 without the arithmetic.
+// 54.5).  That holds below the power limit: such calls without a pause reach
+// it, the clock falls to 1.64 to 1.73 GHz, and one takes 55 to 58 us.  Small
+// matrices are bound by the chain of a launch, the first copies and the join:
+// 1024 x 4096, one vector, 3.3 us, of which a launch of one tile takes 2.7;
+// 6144 x 4096 7.0 us, 6.2 without the arithmetic.  In between, 16 warps an SM
+// do not hide what each waits for: 4096 x 14336 with 16 vectors fills 45% of
+// the issue slots (14.9 us), 4091 x 11008, G = 32, with 5 49% (12.1 us; some
+// SMs have twice the row tiles of others).
 constexpr uint32_t Q4_STEP = 2;                   // tiles a warp takes at a time
 constexpr uint32_t Q4_JOIN_BYTES = 16u * 1024u;   // a CTA's buffer for its cluster's sums
 // Steps in a warp's ring: three where 16 warps leave room for them.
