@@ -153,6 +153,41 @@ __device__ __forceinline__ void ldg256_nc(const void *p, uint4 &a, uint4 &b) {
                  : "l"(p));
 }
 
+// Loads for kernels that are set up while the launch before them still runs, of
+// what that launch may be writing (after the wait for its end).  The read-only
+// path (__ldg) is for data that nothing writes as long as the kernel is there,
+// and such loads may be moved across the wait.
+__device__ __forceinline__ uint32_t ld_after(const uint32_t *p) {
+    uint32_t v;
+    asm volatile("ld.global.u32 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint64_t ld_after(const uint64_t *p) {
+    uint64_t v;
+    asm volatile("ld.global.u64 %0, [%1];" : "=l"(v) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint16_t ld_after(const uint16_t *p) {
+    uint16_t v;
+    asm volatile("ld.global.u16 %0, [%1];" : "=h"(v) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint8_t ld_after(const uint8_t *p) {
+    uint32_t v;
+    asm volatile("ld.global.u8 %0, [%1];" : "=r"(v) : "l"(p));
+    return (uint8_t)v;
+}
+__device__ __forceinline__ uint2 ld_after(const uint2 *p) {
+    uint2 v;
+    asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint4 ld_after(const uint4 *p) {
+    uint4 v;
+    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+
 // acc + w.lo * x.lo, then + w.hi * x.hi: two bf16 pairs, fp32 accumulation
 // (the product of two bf16 values is exact in the fused multiply-add).
 __device__ __forceinline__ float fma2_bf16(uint32_t w, uint32_t x, float acc) {
@@ -174,12 +209,12 @@ __device__ __forceinline__ float fma2_bf16(uint32_t w, uint32_t x, float acc) {
 // on a corrupt table ESC_BAD with length 1.
 __device__ __noinline__ uint32_t resolve_escape(uint32_t x, const uint32_t *__restrict__ g_hier,
                                                 uint32_t n_tables) {
-    uint32_t e = __ldg(g_hier + (x >> 24));
+    uint32_t e = ld_after(g_hier + (x >> 24));
 #pragma unroll 1
     for (int level = 1; level < 4 && (e & LUT_PTR); ++level) {
         const uint32_t child = e & LUT_CHILD_MASK;
         if (child >= n_tables) break;
-        e = __ldg(g_hier + child * 256u + ((x >> (24 - 8 * level)) & 0xFFu));
+        e = ld_after(g_hier + child * 256u + ((x >> (24 - 8 * level)) & 0xFFu));
         if (!(e & LUT_PTR)) {
             const uint32_t l = (e >> LUT_LEN_SHIFT) & 63u;
             if (l > 8u * level && l <= 8u * level + 8u) return e;

@@ -15,6 +15,7 @@
 
 #include <algorithm>
 #include <cstring>
+#include <type_traits>
 
 #include "dfw_lanes.cuh"
 #include "dfw_q4.cuh"
@@ -32,8 +33,8 @@ struct IdSource {
 // Row of token t; false for padding (negative) and for ids past the table,
 // which are also reported.
 __device__ __forceinline__ bool token_row(const IdSource &s, uint32_t t, uint64_t &row, bool report) {
-    const int64_t id = s.wide ? __ldg(static_cast<const long long *>(s.ids) + t)
-                              : (int64_t)__ldg(static_cast<const int *>(s.ids) + t);
+    const int64_t id = s.wide ? (int64_t)ld_after(static_cast<const uint64_t *>(s.ids) + t)
+                              : (int64_t)(int32_t)ld_after(static_cast<const uint32_t *>(s.ids) + t);
     if (id < 0) return false;
     if ((uint64_t)id >= s.rows) {
         if (report) atomicOr(&g_status, ST_INDEX);
@@ -121,7 +122,7 @@ __device__ __forceinline__ void copy_piece(const RowScale &s, const uint16_t *sr
         for (int i = 0; i < 4; ++i) {
             const uint32_t c = c0 + 256u * i + 8u * lane;
             v[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (have && c < end) v[i] = __ldg(reinterpret_cast<const uint4 *>(src + c));
+            if (have && c < end) v[i] = ld_after(reinterpret_cast<const uint4 *>(src + c));
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -129,8 +130,21 @@ __device__ __forceinline__ void copy_piece(const RowScale &s, const uint16_t *sr
             if (c < end) __stcs(reinterpret_cast<uint4 *>(dst + c), have ? scaled8<KIND>(v[i], s) : v[i]);
         }
     } else {
-#pragma unroll 8
-        for (uint32_t c = c0 + lane; c < end; c += 32u) dst[c] = have ? scaled1<KIND>(__ldg(src + c), s) : (uint16_t)0;
+        auto batch = [&](uint32_t at, auto count, bool whole) {  // all loads, then all stores
+            constexpr int U = decltype(count)::value;
+            uint16_t v[U];
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                v[i] = 0;
+                if (have && (whole || at + 32u * i < end)) v[i] = ld_after(src + at + 32u * i);
+            }
+#pragma unroll
+            for (int i = 0; i < U; ++i)
+                if (whole || at + 32u * i < end) dst[at + 32u * i] = have ? scaled1<KIND>(v[i], s) : (uint16_t)0;
+        };
+        uint32_t at = c0 + lane;
+        for (; at + 32u * 7u < end; at += 256u) batch(at, std::integral_constant<int, 8>(), true);
+        for (; at < end; at += 128u) batch(at, std::integral_constant<int, 4>(), false);
     }
 }
 
@@ -293,8 +307,8 @@ __global__ void __launch_bounds__(NT) embed_lanes_rows(const RowsOfLanes p) {
         it.t = unit & 0xFFFFFu;
         it.g = (uint32_t)(w0 / GROUP_SYMS) + (unit >> 20);
         it.from = (int32_t)(w0 % GROUP_SYMS) - (int32_t)(GROUP_SYMS * (unit >> 20));
-        it.s0 = __ldg(prm.group_start + it.g);
-        it.s1 = __ldg(prm.group_start + it.g + 1u);
+        it.s0 = ld_after(prm.group_start + it.g);
+        it.s1 = ld_after(prm.group_start + it.g + 1u);
         return true;
     };
     // lane 0: chunk bits and stream span into slot s / the raw bytes
@@ -416,22 +430,36 @@ __global__ void __launch_bounds__(NT) embed_lanes_rows(const RowsOfLanes p) {
 }
 
 // Rows of a scope with one exponent (no stream): raw bytes joined with it.
-// Bound by memory: 8192 rows of 4096 take 14.7 us (6.9 TB/s, repeated rows from
-// L2), one row 2.7.
+// Bound by memory: 8192 rows of 4096 take 14.3 us (7.0 TB/s, repeated rows from
+// L2), one row 2.1.  (Whole batches without bounds only where they are
+// 16 bytes wide: 4000 rows of 1001 4.7 us with bounds, 5.6 without, one row of
+// 4096 2.4 and 2.1.  Eight accesses in flight: 15.7 us.)
 template <ScaleKind KIND, int V>
 __device__ __forceinline__ void single_row(const RowScale &s, const uint8_t *m, uint32_t E, uint16_t *out, uint32_t dim, uint32_t lane) {
-#pragma unroll 4
-    for (uint32_t c = V * lane; c < dim; c += 32u * V) {
-        if constexpr (V == 8) {
-            const uint2 b = __ldg(reinterpret_cast<const uint2 *>(m + c));
-            uint4 v;
-            join4(E, b.x, v.x, v.y);
-            join4(E, b.y, v.z, v.w);
-            __stcs(reinterpret_cast<uint4 *>(out + c), scaled8<KIND>(v, s));
-        } else {
-            out[c] = scaled1<KIND>(join1(E & 0xFFu, __ldg(m + c)), s);
+    using Bytes = std::conditional_t<V == 8, uint2, uint8_t>;
+    constexpr uint32_t U = 4, STEP = 32u * V;  // accesses in flight
+    auto batch = [&](uint32_t c0, bool whole) {  // all loads, then all stores
+        Bytes b[U];
+#pragma unroll
+        for (uint32_t i = 0; i < U; ++i)
+            if (whole || c0 + i * STEP < dim) b[i] = ld_after(reinterpret_cast<const Bytes *>(m + c0 + i * STEP));
+#pragma unroll
+        for (uint32_t i = 0; i < U; ++i) {
+            const uint32_t c = c0 + i * STEP;
+            if (!whole && c >= dim) break;
+            if constexpr (V == 8) {
+                uint4 v;
+                join4(E, b[i].x, v.x, v.y);
+                join4(E, b[i].y, v.z, v.w);
+                __stcs(reinterpret_cast<uint4 *>(out + c), scaled8<KIND>(v, s));
+            } else {
+                out[c] = scaled1<KIND>(join1(E & 0xFFu, b[i]), s);
+            }
         }
-    }
+    };
+    uint32_t c = V * lane;
+    for (; V == 8 && c + (U - 1u) * STEP < dim; c += U * STEP) batch(c, true);
+    for (; c < dim; c += U * STEP) batch(c, false);
 }
 
 template <int V>
@@ -797,15 +825,15 @@ __global__ void __launch_bounds__(128, 6) grad_reduce(const ReduceParams p) {
     for (uint32_t i = threadIdx.x; i < list; i += 128u) {
         const uint64_t t = (uint64_t)w0 * p.window + i;
         const bool in = t < p.tokens;
-        s_list[i] = in ? __ldg(p.keys + t) : 0xFFFFFFFFu;
-        s_list[list + i] = in ? __ldg(p.pos + t) : 0u;
+        s_list[i] = in ? ld_after(p.keys + t) : 0xFFFFFFFFu;
+        s_list[list + i] = in ? ld_after(p.pos + t) : 0u;
     }
     const uint32_t w = w0 + threadIdx.x / p.tpr;
     const uint32_t col = (blockIdx.x % p.col_blocks * p.tpr + threadIdx.x % p.tpr) * VEC;
     const bool live = w < p.windows && col < p.dim;
     const uint32_t i0 = w * p.window, n = live ? min(p.window, p.tokens - i0) : 0u;
-    const uint32_t prev = live && i0 ? __ldg(p.keys + i0 - 1u) : 0xFFFFFFFFu;
-    const uint32_t next = live && i0 + n < p.tokens ? __ldg(p.keys + i0 + n) : 0xFFFFFFFFu;
+    const uint32_t prev = live && i0 ? ld_after(p.keys + i0 - 1u) : 0xFFFFFFFFu;
+    const uint32_t next = live && i0 + n < p.tokens ? ld_after(p.keys + i0 + n) : 0xFFFFFFFFu;
     __syncthreads();
     if (!live) return;
     const uint32_t *keys = s_list + threadIdx.x / p.tpr * p.window, *pos = keys + list;
@@ -817,7 +845,7 @@ __global__ void __launch_bounds__(128, 6) grad_reduce(const ReduceParams p) {
 #pragma unroll
             for (uint32_t k = 2; k <= JOIN_FEW; ++k) {
                 const uint64_t t = (uint64_t)(w + k) * p.window;
-                on = on && t < p.tokens && __ldg(p.keys + min(t, (uint64_t)p.tokens - 1u)) == tail;
+                on = on && t < p.tokens && ld_after(p.keys + min(t, (uint64_t)p.tokens - 1u)) == tail;
                 more += on;
             }
             const uint32_t at = atomicAdd(p.joins + (more < JOIN_FEW ? 0 : 1), 1u);
@@ -892,14 +920,14 @@ __global__ void __launch_bounds__(256) grad_join(const ReduceParams p) {
     };
     for (uint64_t item = blockIdx.x; item < (uint64_t)many * narrow; item += gridDim.x) {
         const uint32_t w = p.joins[4u + p.windows + (uint32_t)(item / narrow)];
-        const uint32_t col = (uint32_t)(item % narrow) * 32u * VEC + lane * VEC, key = __ldg(p.keys + (uint64_t)(w + 1u) * p.window);
+        const uint32_t col = (uint32_t)(item % narrow) * 32u * VEC + lane * VEC, key = ld_after(p.keys + (uint64_t)(w + 1u) * p.window);
         // the last window that begins with the row: the windows that do come
         // first, so 32 probes at a time narrow it down
         uint32_t last = w + JOIN_FEW, over = p.windows;
         while (over - last > 1u) {
             const uint32_t step = (over - last + 31u) / 32u;
             const uint64_t probe = (uint64_t)last + (uint64_t)step * (lane + 1u);
-            const uint32_t m = __ballot_sync(0xFFFFFFFFu, probe < over && __ldg(p.keys + (probe < over ? probe : w) * p.window) == key);
+            const uint32_t m = __ballot_sync(0xFFFFFFFFu, probe < over && ld_after(p.keys + (probe < over ? probe : w) * p.window) == key);
             last += step * __popc(m);
             over = min(over, last + step);
         }
@@ -925,7 +953,7 @@ __global__ void __launch_bounds__(256) grad_join(const ReduceParams p) {
         const uint32_t entry = p.joins[4u + (uint32_t)(item / wide)], w = entry & 0xFFFFFFu, more = entry >> 24;
         const uint32_t col = ((uint32_t)(item % wide) * 256u + threadIdx.x) * VEC;
         if (col >= p.dim) continue;
-        const uint32_t key = __ldg(p.keys + (uint64_t)(w + 1u) * p.window);
+        const uint32_t key = ld_after(p.keys + (uint64_t)(w + 1u) * p.window);
         float sum[VEC] = {};
         add(sum, w, 1u, col);
         Pack<float, VEC> v[JOIN_FEW - 1];  // (all loads first; those past the row's windows read its last one again)

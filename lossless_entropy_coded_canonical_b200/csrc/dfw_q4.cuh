@@ -539,7 +539,7 @@ __global__ void __launch_bounds__(32 * W, 1) q4_gemv_tiles(const Q4GemvParams a)
                 cp_async16(smem_u32(dst + 16u * c), x + 8u * c);
             } else {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) reinterpret_cast<uint16_t *>(dst + 16u * c)[j] = __ldg(x + 8u * c + j);
+                for (int j = 0; j < 8; ++j) reinterpret_cast<uint16_t *>(dst + 16u * c)[j] = ld_after(x + 8u * c + j);
             }
         }
     }

@@ -683,3 +683,51 @@ def test_rows_of_one_exponent_between_other_calls():
                 kept.append(dfw.embed_rows(x, torch.arange(0, tokens, 50, device="cuda")))
         for n, got in enumerate(kept):
             assert torch.equal(got, want[1 if n % 4 == 2 else 0][n // 4][::50]), (step, n)
+
+
+def test_ids_and_tables_that_the_call_before_writes():
+    """Each call's ids, and some calls' table and gradient rows, come from the
+    launch right before it, which writes over what earlier calls read there."""
+    gen = torch.Generator("cuda").manual_seed(12)
+    rows, dim = 3000, 96
+    u = table(rows * dim, seed=8)
+    coded_table, one = coded(u), coded(table(rows * dim, "single", 9))
+    w = torch.from_numpy(u.view(np.int16)).view(torch.bfloat16).view(rows, dim).cuda()
+    for tokens in (100, 6000):
+        # ids as the bits of bf16 rows: a lookup writes them
+        pools = torch.randint(0, rows, (8 * tokens,), generator=gen, device="cuda").view(torch.bfloat16).view(-1, 4)
+        picks = [torch.randperm(8 * tokens, generator=gen, device="cuda")[:tokens] for _ in range(6)]
+        bits = torch.empty(tokens, 4, dtype=torch.bfloat16, device="cuda")
+        ids = bits.view(torch.int64).view(-1)
+
+        def chain(wait):
+            pause = torch.cuda.synchronize if wait else lambda: None
+            kept = []
+
+            def pick(i):
+                pause()
+                dfw.embed_rows(pools, picks[i], out=bits)
+                pause()
+
+            tab, kept = w.clone(), []
+            for i in range(6):
+                pick(i)
+                kept.append(dfw.embed_lanes(coded_table, ids, dim, scale=2.0))
+                pick((i + 1) % 6)
+                kept.append(dfw.embed_lanes(one, ids, dim))
+                pick((i + 2) % 6)
+                x = dfw.embed_rows(tab, ids, scale=0.5)
+                pause()
+                kept.append(dfw.embed_rows(x, ids.clamp(max=tokens - 1)))
+                pick((i + 3) % 6)
+                kept.append(dfw.embed_grad(ids, x, rows))
+                pick((i + 4) % 6)
+                dfw.embed_grad(ids, x, rows, out=tab, accumulate=True)
+                pause()
+                kept.append(dfw.embed_rows(tab, picks[0][:200].clamp(max=rows - 1)))
+            torch.cuda.synchronize()
+            return kept
+
+        want = chain(True)
+        for _ in range(4):
+            assert all(torch.equal(a, b) for a, b in zip(chain(False), want))
