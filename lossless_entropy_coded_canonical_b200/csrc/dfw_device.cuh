@@ -204,9 +204,9 @@ __device__ __forceinline__ float fma2_bf16(uint32_t w, uint32_t x, float acc) {
 // --------------------------------------------------------------- decoding
 
 // A codeword longer than the fast table's key: walk the byte-keyed hierarchy
-// (global memory, read-only path).  x holds the 32 stream bits from the
-// codeword's first bit.  Returns a hierarchy leaf (symbol, total length), or
-// on a corrupt table ESC_BAD with length 1.
+// (global memory).  x holds the 32 stream bits from the codeword's first bit.
+// Returns a hierarchy leaf (symbol, total length), or on a corrupt table
+// ESC_BAD with length 1.
 __device__ __noinline__ uint32_t resolve_escape(uint32_t x, const uint32_t *__restrict__ g_hier,
                                                 uint32_t n_tables) {
     uint32_t e = ld_after(g_hier + (x >> 24));
